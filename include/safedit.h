@@ -69,7 +69,10 @@ typedef enum {
   SAFEDIT_BOOL = 3, /* one byte, nonzero = true */
   SAFEDIT_I32 = 4,
   SAFEDIT_F64 = 5,
-  SAFEDIT_U8 = 6
+  SAFEDIT_U8 = 6,
+  SAFEDIT_I8 = 7,  /* codes of an 8-bit state only */
+  SAFEDIT_E4M3 = 8 /* codes of an 8-bit state only: sign, 4 exponent bits of
+                      bias 7, 3 mantissa bits, largest 448, no infinity */
 } safedit_dtype;
 
 typedef struct {
@@ -319,6 +322,141 @@ safedit_status safedit_gather_rows(const safedit_tensor *src,
                                    int32_t n_idx, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Rotary positions on several axes (time or text, height, width).  The pages
+ * have no counterpart: their backbones rotate Q and K between projection and
+ * attention, and an SRSU step does it for the S rows at their own tokens'
+ * positions.
+ *
+ * A row's first axis_dim[0] elements turn by its position on axis 0, the next
+ * axis_dim[1] by that on axis 1, and so on; elements behind the last segment
+ * are copied.  Pair m of a segment of s elements turns by
+ *   a = pos[b, i, axis] * theta[axis]^(-2 m / s),
+ *   (x, y) -> (x cos a - y sin a, x sin a + y cos a)       inverse == 0
+ *   (x, y) -> (x cos a + y sin a, y cos a - x sin a)       inverse == 1
+ * where (x, y) are elements 2m and 2m + 1 of the segment (halves == 0) or m
+ * and m + s/2 (halves == 1).  inverse == 1 undoes the rotation; it is also
+ * its transpose, so it takes the gradient of the rotated rows to that of the
+ * rows.  Angles are reduced in fp64, the rotation is in fp32, rounded once.
+ */
+typedef struct {
+  int32_t n_axes;      /* 1..4                                             */
+  int32_t halves;      /* 0: neighbouring pairs, 1: pairs half a segment apart */
+  int32_t inverse;     /* 0 or 1                                           */
+  int32_t axis_dim[4]; /* even (halves == 0) or a multiple of 8 (halves == 1) */
+  double theta[4];     /* > 0, the base of the axis' frequencies           */
+} safedit_rope;
+
+/* For t < n_tensors, r < n, i = d_idx ? d_idx[r] : r (the token):
+ *   dst[t][b,h,(dst_indexed ? i : r),:] =
+ *       src[t][b,h,(src_indexed ? i : r),:] rotated at pos[b,i,:]
+ * with n = n_idx where d_idx is given and the source's row count otherwise.
+ * src_indexed == 1 gathers rows, dst_indexed == 1 scatters them into a state
+ * whose other rows are untouched (d_idx entries must then be unique: checked
+ * only in the debug index-check mode).  Both need d_idx.
+ *
+ * src[t], dst[t] [B,H_t,rows,d], all of one type: bf16, f16 or f32; d a
+ * multiple of 8, at most 256; d contiguous, other strides multiples of 16
+ * bytes, data 16-byte aligned.  A compact side has n rows.  1 <= n_tensors
+ * <= 4, one launch for all (Q and K share their angles).  pos [B or 1,
+ * tokens, n_axes] i32 or f32, any strides, |pos| <= 2^31.  A tensor may be
+ * rotated in place (src[t] == dst[t], the same strides, src_indexed ==
+ * dst_indexed); otherwise src and dst must not overlap.  An index outside the
+ * tokens, or outside the rows of an indexed side, sets SAFEDIT_ERR_INDEX and
+ * its row is skipped.
+ */
+safedit_status safedit_rope_rows(const safedit_tensor *src,
+                                 const safedit_tensor *dst, int32_t n_tensors,
+                                 const safedit_tensor *pos,
+                                 const safedit_rope *rope, const int32_t *d_idx,
+                                 int32_t n_idx, int32_t src_indexed,
+                                 int32_t dst_indexed, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit state: cached K and V rows as 8-bit codes with an f32 scale for
+ * each block of `block` consecutive rows of a head (half the bytes of the
+ * bf16 state).  The pages have no counterpart: a storage form of the cached
+ * context state of [P1 방법론 3 / P4 Metodologia 3].
+ *
+ * A stored element stands for code * scale, with
+ *   scale = m / qmax,  code = x qmax / m rounded to the nearest code (ties to
+ *   even),  m = the largest |x| of the block's rows over the head's width,
+ * qmax = 448 (e4m3) or 127 (int8); m = 0 takes scale 1, and 0 < m < 2^-100
+ * counts as 2^-100.  x is the source element, rotated first (in fp32, as
+ * safedit_rope_rows does, with no rounding in between) in the tensors with
+ * host_rotate[t] == 1.
+ *
+ * For t < n_tensors, r < n, i = d_idx ? d_idx[r] : r:
+ *   state row row0 + r = src[t][b,h,(src_indexed ? i : r),:]  at pos[b,i,:]
+ * with n = n_idx where d_idx is given and the source's row count otherwise.
+ * A call owns the blocks that it writes: row0 is a multiple of `block` (else
+ * SAFEDIT_ERR_ALIGNMENT), row0 + n <= N, and the rows of the last block
+ * behind row0 + n get zero codes.  Attention does not depend on the order of
+ * the keys, so a state may keep the S rows in blocks of their own (rewritten
+ * by each SRSU step) and the C rows behind them (rewritten by anchors), with
+ * key_pad = -inf on the zero rows between.
+ *
+ * src[t] [B,H_t,rows,d] bf16, f16 or f32 (one type), layout as in
+ * safedit_rope_rows, d in {64, 96, 128}.  codes[t] [B,H_t,N,d] int8 or e4m3
+ * (one type for all), d contiguous, other strides multiples of 16.  scales[t]
+ * [B,H_t,ceil(N/block)] f32, blocks contiguous.  block in {16, 32, 64, 128}.
+ * host_rotate: n_tensors values on the host, or NULL (none); pos and rope
+ * (inverse == 0) are needed where one is 1 and may be NULL otherwise.
+ * 1 <= n_tensors <= 4, one launch for all.  An index outside the source rows
+ * (src_indexed) or the tokens (rotated) sets SAFEDIT_ERR_INDEX and its row
+ * gets zero codes.  A NaN or infinity in the rows sets
+ * SAFEDIT_ERR_INVALID_ARG; it is stored as 0 or as the largest code of its
+ * sign and leaves the block's scale to the finite elements.
+ */
+safedit_status safedit_state8_store(const safedit_tensor *src,
+                                    const safedit_tensor *codes,
+                                    const safedit_tensor *scales,
+                                    int32_t n_tensors, int32_t block,
+                                    int64_t row0, const int32_t *d_idx,
+                                    int32_t n_idx, int32_t src_indexed,
+                                    const int32_t *host_rotate,
+                                    const safedit_tensor *pos,
+                                    const safedit_rope *rope, void *stream);
+
+/* ------------------------------------------------------------------------
+ * SRSU subset attention and CAR dense anchor over an 8-bit state.
+ *
+ * For r in [0, n_rows), i = d_idx[r] (i = r when d_idx is NULL):
+ *   out_r = sum_j softmax_j( scale * q[b,h,i,:] . K[b,h,j,:] + key_pad[b,j] )
+ *           V[b,h,j,:]
+ * over all Nk keys, K = k8 * k_scale of the key's block, V = v8 * v_scale.
+ * q, d_idx, n_idx, key_pad, scale, out and out_scattered as in
+ * safedit_attn_subset (there is no dense bias).  k8, v8 [B,H,Nk,d] codes of
+ * one type, k_scale, v_scale [B,H,ceil(Nk/block)] f32, block in {16,32,64,128},
+ * laid out as safedit_state8_store writes them.  Codes are widened exactly
+ * and the sums are fp32; the probabilities alone are rounded (to f16).
+ *
+ * A key with key_pad == -inf carries no weight whatever its codes and scales
+ * hold.  The other keys' scales must be finite, k_scale >= 0, v_scale > 0,
+ * and those of one (b, h) slice of V within a factor of 2^64 of each other;
+ * otherwise SAFEDIT_ERR_INVALID_ARG is set and the rows are unspecified.
+ * A row whose every key is masked sets SAFEDIT_ERR_MASKED_ROW and gets zeros.
+ *
+ * d_workspace / workspace_bytes as in safedit_attn_subset_ws: at least
+ * safedit_attn_subset_state8_workspace_size(...) bytes for this call on the
+ * current device (the keys of a call with few rows are split over the SMs and
+ * the parts joined afterwards), NULL where that is 0.
+ */
+safedit_status safedit_attn_subset_state8(
+    const safedit_tensor *q, const safedit_tensor *k8,
+    const safedit_tensor *k_scale, const safedit_tensor *v8,
+    const safedit_tensor *v_scale, int32_t block, const int32_t *d_idx,
+    int32_t n_idx, const safedit_tensor *key_pad, float scale,
+    const safedit_tensor *out, int32_t out_scattered, void *d_workspace,
+    size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of safedit_attn_subset_state8 on the current device for
+ * batch x heads slices of n_rows query rows over n_keys keys.  Host only, no
+ * launch; invalid sizes give 0. */
+size_t safedit_attn_subset_state8_workspace_size(int64_t batch, int64_t heads,
+                                                 int64_t n_rows, int64_t n_keys,
+                                                 int32_t head_dim);
+
+/* ------------------------------------------------------------------------
  * Sensitivity-weighted CFG.  [P1 방법론 4 / P4 Metodologia 4]:
  *   gamma_i = gamma_ctx + (gamma_sens - gamma_ctx) * s_i,
  * applied to the prediction after the forward pass; [P3 B.2] spatial CFG.
@@ -404,8 +542,9 @@ uint64_t safedit_kernel_launch_count(void);
 uint64_t safedit_debug_set_wait_limit_ns(uint64_t ns);
 
 /* Debug knob: with `on` non-zero, every call that writes rows through an
- * index vector (safedit_scatter_state, safedit_attn_subset with
- * out_scattered == 1, safedit_gemm_bias_act with d_idx_out) first launches a
+ * index vector (safedit_scatter_state, safedit_attn_subset and
+ * safedit_attn_subset_state8 with out_scattered == 1, safedit_gemm_bias_act
+ * with d_idx_out, safedit_rope_rows with dst_indexed == 1) first launches a
  * check of that vector on the same stream: an entry out of range or equal to
  * an earlier one sets SAFEDIT_ERR_INDEX in the device status word (the
  * scattering kernel still runs; its output is then unspecified).  The check

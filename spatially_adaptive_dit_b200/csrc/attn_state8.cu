@@ -1,0 +1,530 @@
+// attn_state8.cu -- attention of gathered query rows over an 8-bit state.
+#include <cmath>
+
+#include "attn_state8.cuh"
+#include "state8.cuh"
+
+namespace sd {
+
+// ------------------------------------------------------------- few rows
+// One CTA: 16 query rows (one warp-level matrix tile) of a (b, h) slice and a
+// range of the keys, its warps taking groups of 16 keys in turn.  Bound by
+// reading the state once.  Codes go from global memory into the registers of
+// the warp-level multiplication with no shared memory between: the order of a
+// row's elements inside the product is free as long as both operands agree,
+// so each lane loads runs of 16 (8, 4) consecutive bytes and hands them out
+// as if they were the tile's scattered elements.
+//   scores: lane (g = lane / 4, t = lane % 4) loads bytes [t D/4, (t+1) D/4) of
+//     keys 4 (g / 2) + g % 2 and two further; step s multiplies bytes 4 s..+3.
+//   values: it loads, of keys 4 t..4 t + 3 (whose weights it holds), the
+//     elements of column group g, and interleaves them by bytes.
+constexpr int kRowWarps = 4;
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Column of element i (0 <= i < D / 8) of column group g.
+template <int D>
+__device__ __forceinline__ constexpr int value_col(int g, int i) {
+  if constexpr (D == 96) return i < 8 ? g * 8 + i : 64 + g * 4 + (i - 8);
+  else return g * (D / 8) + i;
+}
+
+template <int D>
+__device__ __forceinline__ void load_key_run(uint32_t (&w)[D / 16], const uint8_t* at) {
+  if constexpr (D == 96) {
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(at) + e);
+      w[2 * e] = x.x, w[2 * e + 1] = x.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(at) + e);
+      w[4 * e] = x.x, w[4 * e + 1] = x.y, w[4 * e + 2] = x.z, w[4 * e + 3] = x.w;
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_value_run(uint32_t (&w)[D / 32], const uint8_t* row, int g) {
+  if constexpr (D == 128) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + g * 16));
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(row + g * 8));
+    w[0] = x.x, w[1] = x.y;
+    if constexpr (D == 96) w[2] = __ldg(reinterpret_cast<const uint32_t*>(row + 64 + g * 4));
+  }
+}
+
+template <int D>
+struct RowGroup {  // the codes of 16 keys as one lane holds them
+  uint32_t k[2][D / 16];
+  uint32_t v[4][D / 32];
+  float ks, vs;
+  float pad[4];
+};
+
+template <int D, bool PAD, bool E4M3>
+__global__ void __launch_bounds__(kRowWarps * 32) attn_state8_rows_kernel(const __grid_constant__ State8Params p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int NT = D / 8;  // column tiles of the output
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int split = blockIdx.x, tile = blockIdx.y, bh = blockIdx.z;
+  const int b = bh / p.H, h = bh - b * p.H;
+  const int ng = (p.Nk + 15) >> 4;
+  const int g_lo = int(int64_t(ng) * split / p.n_split), g_hi = int(int64_t(ng) * (split + 1) / p.n_split);
+
+  // ---- query rows g and g + 8 of the tile, f16, in the order of the key runs
+  uint32_t aq[D / 16][4];
+  float undo[2];
+  int my_q[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = tile * 16 + g + 8 * e;
+    my_q[e] = -1;
+    if (r < p.n_rows) {
+      my_q[e] = p.idx ? __ldg(p.idx + r) : r;
+      if (my_q[e] < 0 || my_q[e] >= p.Nq) {
+        set_status(p.status, SAFEDIT_ERR_INDEX);
+        my_q[e] = -1;
+      }
+    }
+    uint32_t raw[D / 8];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) raw[c] = 0u;
+    if (my_q[e] >= 0) {
+      const uint2* src = reinterpret_cast<const uint2*>(p.q + b * p.q_sb + h * p.q_sh + int64_t(my_q[e]) * p.q_sr +
+                                                        t * (D / 4));
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const uint2 x = __ldg(src + c);
+        raw[2 * c] = x.x, raw[2 * c + 1] = x.y;
+      }
+    }
+    uint32_t m = 0u;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) m = max(m, max((raw[c] << 16) & 0x7FFF0000u, raw[c] & 0x7FFF0000u));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const float f = query_factor(m, p.scale_log2, undo[e]);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      aq[s][e] = pack_f16x2(__uint_as_float(raw[2 * s] << 16) * f, __uint_as_float(raw[2 * s] & 0xFFFF0000u) * f);
+      aq[s][e + 2] =
+          pack_f16x2(__uint_as_float(raw[2 * s + 1] << 16) * f, __uint_as_float(raw[2 * s + 1] & 0xFFFF0000u) * f);
+    }
+  }
+
+  const uint8_t* kb = p.k + b * p.k_sb + h * p.k_sh + t * (D / 4);
+  const uint8_t* vb = p.v + b * p.v_sb + h * p.v_sh;
+  const float* ksb = p.ks + b * p.ks_sb + h * p.ks_sh;
+  const float* vsb = p.vs + b * p.vs_sb + h * p.vs_sh;
+  const float* padb = PAD ? p.pad + b * p.pad_sb : nullptr;
+  const int key_k = 4 * (g >> 1) + (g & 1);  // this lane's first key of a score tile
+
+  // codes past the last key are zero, and so are those of masked keys: what
+  // they hold (NaN codes too) does not reach a product
+  auto fetch = [&](RowGroup<D>& x, int grp) {
+    const int key0 = grp * 16;
+    x.ks = __ldg(ksb + (key0 >> p.block_log2));
+    x.vs = __ldg(vsb + (key0 >> p.block_log2));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) x.k[e][c] = 0u;
+      if (key0 + key_k + 2 * e < p.Nk) load_key_run<D>(x.k[e], kb + int64_t(key0 + key_k + 2 * e) * p.k_sr);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = key0 + 4 * t + e;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) x.v[e][c] = 0u;
+      if (key < p.Nk) load_value_run<D>(x.v[e], vb + int64_t(key) * p.v_sr, g);
+      if constexpr (PAD) x.pad[e] = key < p.Nk ? __ldg(padb + key) : -INFINITY;
+    }
+  };
+
+  float o[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float lv_lo = INFINITY, lv_hi = -INFINITY;
+  bool bad = false;
+
+  RowGroup<D> next;
+  int grp = g_lo + warp;
+  if (grp < g_hi) fetch(next, grp);
+  for (; grp < g_hi; grp += kRowWarps) {
+    RowGroup<D> x = next;
+    if (grp + kRowWarps < g_hi) fetch(next, grp + kRowWarps);
+    const int key0 = grp * 16;
+    if constexpr (PAD) {  // a group of masked keys alone: its scales may be anything
+      bool live = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) live |= x.pad[e] != -INFINITY;
+      if (!__any_sync(0xffffffffu, live)) continue;
+    }
+    const float lv = __log2f(x.vs);
+    bad |= !(x.ks >= 0.f && x.ks < INFINITY && x.vs > 0.f && x.vs < INFINITY);
+    lv_lo = fminf(lv_lo, lv);
+    lv_hi = fmaxf(lv_hi, lv);
+    float s[2][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      s[e][0] = s[e][1] = s[e][2] = s[e][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const uint32_t w = bias_codes<E4M3>(x.k[e][c]);
+        mma_16816(s[e], aq[c], widen_lo<E4M3>(w), widen_hi<E4M3>(w));
+      }
+    }
+    // weights of rows g and g + 8, keys key0 + 4 t + {0, 1, 2, 3}
+    uint32_t ap[4];
+    bool up = false;
+    float a[2][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float f = undo[r] * x.ks;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int key = key0 + 4 * t + e;
+        const float raw = s[e >> 1][2 * r + (e & 1)];
+        if constexpr (PAD) {
+          a[r][e] = x.pad[e] == -INFINITY ? -INFINITY : fmaf(raw, f, pad_log2(x.pad[e]));
+        } else {
+          a[r][e] = key < p.Nk ? raw * f : -INFINITY;
+        }
+      }
+      const float top = fmaxf(fmaxf(a[r][0], a[r][1]), fmaxf(a[r][2], a[r][3])) + lv;
+      up |= top > m[r] + 8.f;
+    }
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float top = fmaxf(fmaxf(a[r][0], a[r][1]), fmaxf(a[r][2], a[r][3])) + lv;
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (top > m[r]) {
+          const float al = ex2_approx(m[r] - top);  // 0 from m = -inf
+          m[r] = top;
+          l[r] *= al;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            o[i][2 * r] *= al;
+            o[i][2 * r + 1] *= al;
+          }
+        }
+      }
+    }
+    const float inv = ex2_approx(-lv);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float mm = m[r] == -INFINITY ? 0.f : m[r];
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = ex2_approx((a[r][e] - mm) + lv);
+      l[r] = fmaf((w[0] + w[1]) + (w[2] + w[3]), inv, l[r]);
+      ap[r] = pack_f16x2(w[0], w[1]);
+      ap[r + 2] = pack_f16x2(w[2], w[3]);
+    }
+    if constexpr (PAD) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          if (x.pad[e] == -INFINITY) x.v[e][c] = 0u;
+    }
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = bias_codes<E4M3>(x.v[e][c]);
+      // bytes of keys (0, 1) and (2, 3) side by side, column by column
+      const uint32_t a0 = __byte_perm(w[0], w[1], 0x5140), a1 = __byte_perm(w[0], w[1], 0x7362);
+      const uint32_t b0 = __byte_perm(w[2], w[3], 0x5140), b1 = __byte_perm(w[2], w[3], 0x7362);
+      mma_16816(o[4 * c], ap, widen_lo<E4M3>(a0), widen_lo<E4M3>(b0));
+      mma_16816(o[4 * c + 1], ap, widen_hi<E4M3>(a0), widen_hi<E4M3>(b0));
+      mma_16816(o[4 * c + 2], ap, widen_lo<E4M3>(a1), widen_lo<E4M3>(b1));
+      mma_16816(o[4 * c + 3], ap, widen_hi<E4M3>(a1), widen_hi<E4M3>(b1));
+    }
+  }
+
+  // ---- the warps' results joined in shared memory
+  __shared__ float sm_m[kRowWarps][16], sm_l[kRowWarps][16], sm_range[kRowWarps][2];
+  __shared__ float sm_o[16][D];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    if (t == 0) sm_m[warp][g + 8 * r] = m[r], sm_l[warp][g + 8 * r] = l[r];
+  }
+  if (lane == 0) sm_range[warp][0] = lv_lo, sm_range[warp][1] = lv_hi;
+  if (bad) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
+  for (int e = threadIdx.x; e < 16 * D; e += kRowWarps * 32) (&sm_o[0][0])[e] = 0.f;
+  __syncthreads();
+  float mx[2], lx[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int rr = g + 8 * r;
+    mx[r] = -INFINITY, lx[r] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) mx[r] = fmaxf(mx[r], sm_m[w][rr]);
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w)
+      if (sm_m[w][rr] != -INFINITY) lx[r] = fmaf(ex2_approx(sm_m[w][rr] - mx[r]), sm_l[w][rr], lx[r]);
+    m[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - mx[r]);  // this warp's factor
+  }
+  for (int w = 0; w < kRowWarps; ++w) {  // one warp after another: the sum's order is fixed
+    if (warp == w) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          sm_o[g + 8 * r][value_col<D>(2 * t, i)] += o[i][2 * r] * m[r];
+          sm_o[g + 8 * r][value_col<D>(2 * t + 1, i)] += o[i][2 * r + 1] * m[r];
+        }
+    }
+    __syncthreads();
+  }
+  for (int w = 0; w < kRowWarps; ++w) lv_lo = fminf(lv_lo, sm_range[w][0]), lv_hi = fmaxf(lv_hi, sm_range[w][1]);
+  const int64_t rec = (int64_t(bh) * p.n_tiles + tile) * p.n_split + split;
+  if (p.n_split > 1) {
+    const PartView pv = part_view(p, rec, D);
+    for (int e = threadIdx.x; e < 16 * D; e += kRowWarps * 32) pv.o[e] = (&sm_o[0][0])[e];
+    if (warp == 0 && t == 0) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) pv.ml[(g + 8 * r) * 2] = mx[r], pv.ml[(g + 8 * r) * 2 + 1] = lx[r];
+    }
+    if (threadIdx.x == 0) pv.range[0] = lv_lo, pv.range[1] = lv_hi;
+    return;
+  }
+  if (threadIdx.x == 0 && lv_hi - lv_lo > kScaleSpread) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
+  if (warp == 0 && t == 0) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) sm_l[0][g + 8 * r] = lx[r], sm_m[0][g + 8 * r] = __int_as_float(my_q[r]);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 16 * D / 2; e += kRowWarps * 32) {
+    const int rr = e / (D / 2), c = (e - rr * (D / 2)) * 2;
+    const int qi = __float_as_int(sm_m[0][rr]);
+    if (qi < 0) continue;
+    const float ls = sm_l[0][rr];
+    if (ls == 0.f && c == 0) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
+    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    const int64_t orow = p.out_scattered ? int64_t(qi) : int64_t(tile * 16 + rr);
+    *reinterpret_cast<uint32_t*>(p.out + b * p.o_sb + h * p.o_sh + orow * p.o_sr + c) =
+        pack_bf16x2(sm_o[rr][c] * inv, sm_o[rr][c + 1] * inv);
+  }
+}
+
+// ------------------------------------------------------------- parts joined
+// One CTA for each query row: m = max m_i, out = sum 2^(m_i - m) O_i /
+// sum 2^(m_i - m) l_i over the row's parts, in their order.
+template <int D>
+__global__ void __launch_bounds__(D) attn_state8_join_kernel(const __grid_constant__ State8Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int r = blockIdx.x, bh = blockIdx.y, c = threadIdx.x;
+  const int b = bh / p.H, h = bh - b * p.H;
+  const int tile = r / p.tile_rows, rr = r - tile * p.tile_rows;
+  const int qi = p.idx ? __ldg(p.idx + r) : r;
+  if (qi < 0 || qi >= p.Nq) return;  // reported by the attention kernel
+  const int64_t rec0 = (int64_t(bh) * p.n_tiles + tile) * p.n_split;
+  float m = -INFINITY, lv_lo = INFINITY, lv_hi = -INFINITY;
+  for (int s = 0; s < p.n_split; ++s) {
+    const PartView v = part_view(p, rec0 + s, D);
+    m = fmaxf(m, v.ml[rr * 2]);
+    lv_lo = fminf(lv_lo, v.range[0]), lv_hi = fmaxf(lv_hi, v.range[1]);
+  }
+  float l = 0.f, acc = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.n_split; ++s) {
+    const PartView v = part_view(p, rec0 + s, D);
+    const float ms = v.ml[rr * 2];
+    const float w = ms == -INFINITY ? 0.f : ex2_approx(ms - m);
+    l = fmaf(w, v.ml[rr * 2 + 1], l);
+    if (w != 0.f) acc = fmaf(w, v.o[rr * D + c], acc);
+  }
+  if (c == 0) {
+    if (lv_hi - lv_lo > kScaleSpread) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
+    if (l == 0.f) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
+  }
+  const int64_t orow = p.out_scattered ? int64_t(qi) : int64_t(r);
+  p.out[b * p.o_sb + h * p.o_sh + orow * p.o_sr + c] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
+}
+
+// ------------------------------------------------------------- plan
+struct State8Plan {
+  int tile_rows = 16, n_tiles = 0, n_split = 1;
+  int64_t n_records = 0;
+  size_t ws_bytes = 0;
+};
+
+static int state8_sms() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 148;
+  return sms;
+}
+
+static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int sms) {
+  State8Plan pl;
+  pl.n_tiles = int((n_rows + 15) / 16);
+  const int64_t ctas = pl.n_tiles * BH;
+  // three CTAs on an SM, each warp at least two groups of 16 keys
+  int64_t split = ctas > 0 ? int64_t(sms) * 3 / ctas : 1;
+  const int64_t most = (Nk + 16 * kRowWarps * 2 - 1) / (16 * kRowWarps * 2);
+  if (split > most) split = most;
+  if (split < 1) split = 1;
+  pl.n_split = int(split);
+  if (split > 1) {
+    pl.n_records = ctas * split;
+    pl.ws_bytes = part_floats(pl.n_records, pl.tile_rows, D) * sizeof(float);
+  }
+  return pl;
+}
+
+template <int D>
+static safedit_status launch_join(const State8Params& p, int64_t BH, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.n_rows), unsigned(BH));
+  cfg.blockDim = dim3(D);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_state8_join_kernel<D>, p) != cudaSuccess) return SAFEDIT_ERR_CUDA;
+  return after_launch(1);
+}
+
+template <int D, bool PAD, bool E4M3>
+static safedit_status launch_state8(const State8Params& p, int64_t BH, cudaStream_t s) {
+  attn_state8_rows_kernel<D, PAD, E4M3>
+      <<<dim3(unsigned(p.n_split), unsigned(p.n_tiles), unsigned(BH)), kRowWarps * 32, 0, s>>>(p);
+  safedit_status st = after_launch(1);
+  if (st != SAFEDIT_OK || p.n_split == 1) return st;
+  return launch_join<D>(p, BH, s);
+}
+
+template <int D>
+static safedit_status dispatch_state8(const State8Params& p, int64_t BH, bool e4m3, cudaStream_t s) {
+  if (p.pad) return e4m3 ? launch_state8<D, true, true>(p, BH, s) : launch_state8<D, true, false>(p, BH, s);
+  return e4m3 ? launch_state8<D, false, true>(p, BH, s) : launch_state8<D, false, false>(p, BH, s);
+}
+
+static safedit_status check_rows16(const safedit_tensor* t) {
+  const safedit_status st = check_tensor(t, 4);
+  if (st != SAFEDIT_OK) return st;
+  if (t->dtype != SAFEDIT_BF16) return SAFEDIT_ERR_DTYPE;
+  if (t->strides[3] != 1 || !aligned16(t->data)) return SAFEDIT_ERR_ALIGNMENT;
+  for (int k = 0; k < 3; ++k)
+    if (t->strides[k] % 8 != 0 || t->strides[k] < 0) return SAFEDIT_ERR_ALIGNMENT;
+  return SAFEDIT_OK;
+}
+
+}  // namespace sd
+
+using namespace sd;
+
+extern "C" safedit_status safedit_attn_subset_state8(const safedit_tensor* q, const safedit_tensor* k8,
+                                                     const safedit_tensor* k_scale, const safedit_tensor* v8,
+                                                     const safedit_tensor* v_scale, int32_t block,
+                                                     const int32_t* d_idx, int32_t n_idx,
+                                                     const safedit_tensor* key_pad, float scale,
+                                                     const safedit_tensor* out, int32_t out_scattered,
+                                                     void* d_workspace, size_t workspace_bytes, void* stream) {
+  safedit_status st;
+  if ((st = check_rows16(q)) != SAFEDIT_OK) return st;
+  if ((st = check_codes(k8)) != SAFEDIT_OK) return st;
+  if ((st = check_codes(v8)) != SAFEDIT_OK) return st;
+  if (!state8_block_ok(block)) return SAFEDIT_ERR_UNSUPPORTED;
+  if ((st = check_scales(k_scale, k8, block)) != SAFEDIT_OK) return st;
+  if ((st = check_scales(v_scale, v8, block)) != SAFEDIT_OK) return st;
+  if ((st = check_rows16(out)) != SAFEDIT_OK) return st;
+  if (k8->dtype != v8->dtype) return SAFEDIT_ERR_DTYPE;
+  const int64_t B = q->dims[0], H = q->dims[1], Nq = q->dims[2], D = q->dims[3], Nk = k8->dims[2];
+  for (const safedit_tensor* t : {k8, v8})
+    if (t->dims[0] != B || t->dims[1] != H || t->dims[3] != D || t->dims[2] != Nk) return SAFEDIT_ERR_SHAPE;
+  if (D != 64 && D != 96 && D != 128) return SAFEDIT_ERR_UNSUPPORTED;
+  if (Nk < 1 || Nq > INT32_MAX || Nk > INT32_MAX - 256 || B * H > 65535) return SAFEDIT_ERR_SHAPE;
+  if (out_scattered != 0 && out_scattered != 1) return SAFEDIT_ERR_INVALID_ARG;
+  if (d_idx && n_idx < 0) return SAFEDIT_ERR_INVALID_ARG;
+  const int64_t n_rows = d_idx ? n_idx : Nq;
+  if (out->dims[0] != B || out->dims[1] != H || out->dims[3] != D) return SAFEDIT_ERR_SHAPE;
+  if (out->dims[2] != (out_scattered ? Nq : n_rows)) return SAFEDIT_ERR_SHAPE;
+  if ((n_rows + 15) / 16 > 65535) return SAFEDIT_ERR_SHAPE;
+  State8Params p{};
+  if (key_pad) {
+    if ((st = check_tensor(key_pad, 2)) != SAFEDIT_OK) return st;
+    if (key_pad->dtype != SAFEDIT_F32) return SAFEDIT_ERR_DTYPE;
+    if (key_pad->dims[0] != B || key_pad->dims[1] != Nk) return SAFEDIT_ERR_SHAPE;
+    if (key_pad->strides[1] != 1 || key_pad->strides[0] % 4 != 0 || key_pad->strides[0] < 0 ||
+        !aligned16(key_pad->data))
+      return SAFEDIT_ERR_ALIGNMENT;
+    p.pad = static_cast<const float*>(key_pad->data);
+    p.pad_sb = key_pad->strides[0];
+  }
+  const State8Plan pl = plan_state8(n_rows, B * H, Nk, int(D), state8_sms());
+  if (pl.ws_bytes > 0) {
+    if (!d_workspace || workspace_bytes < pl.ws_bytes) return SAFEDIT_ERR_INVALID_ARG;
+    if (!aligned16(d_workspace)) return SAFEDIT_ERR_ALIGNMENT;
+  }
+  if (n_rows == 0 || B * H == 0) return SAFEDIT_OK;
+  p.q = static_cast<const __nv_bfloat16*>(q->data);
+  p.q_sb = q->strides[0], p.q_sh = q->strides[1], p.q_sr = q->strides[2];
+  p.k = static_cast<const uint8_t*>(k8->data);
+  p.k_sb = k8->strides[0], p.k_sh = k8->strides[1], p.k_sr = k8->strides[2];
+  p.v = static_cast<const uint8_t*>(v8->data);
+  p.v_sb = v8->strides[0], p.v_sh = v8->strides[1], p.v_sr = v8->strides[2];
+  p.ks = static_cast<const float*>(k_scale->data);
+  p.ks_sb = k_scale->strides[0], p.ks_sh = k_scale->strides[1];
+  p.vs = static_cast<const float*>(v_scale->data);
+  p.vs_sb = v_scale->strides[0], p.vs_sh = v_scale->strides[1];
+  p.block_log2 = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+  p.idx = d_idx;
+  p.n_rows = int(n_rows);
+  p.Nq = int(Nq);
+  p.Nk = int(Nk);
+  p.H = int(H);
+  p.scale_log2 = ((scale > 0.f) ? scale : 1.0f / std::sqrt(float(D))) * kLog2eF;
+  p.out = static_cast<__nv_bfloat16*>(out->data);
+  p.o_sb = out->strides[0], p.o_sh = out->strides[1], p.o_sr = out->strides[2];
+  p.out_scattered = out_scattered;
+  p.wait_limit = wait_limit_ns();
+  p.n_split = pl.n_split;
+  p.tile_rows = pl.tile_rows;
+  p.n_tiles = pl.n_tiles;
+  p.n_records = pl.n_records;
+  p.part = static_cast<float*>(d_workspace);
+  p.status = status_ptr();
+  if (!p.status) return SAFEDIT_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d_idx && out_scattered && index_check_enabled() &&
+      (st = launch_index_check(d_idx, int32_t(n_rows), Nq, p.status, s)) != SAFEDIT_OK)
+    return st;
+  const bool e4m3 = k8->dtype == SAFEDIT_E4M3;
+  switch (D) {
+    case 64: return dispatch_state8<64>(p, B * H, e4m3, s);
+    case 96: return dispatch_state8<96>(p, B * H, e4m3, s);
+    default: return dispatch_state8<128>(p, B * H, e4m3, s);
+  }
+}
+
+extern "C" size_t safedit_attn_subset_state8_workspace_size(int64_t batch, int64_t heads, int64_t n_rows,
+                                                            int64_t n_keys, int32_t head_dim) {
+  if (batch <= 0 || heads <= 0 || n_rows <= 0 || n_keys <= 0) return 0;
+  if (head_dim != 64 && head_dim != 96 && head_dim != 128) return 0;
+  if (batch > 65535 || heads > 65535 || batch * heads > 65535 || n_keys > INT32_MAX - 256 ||
+      (n_rows + 15) / 16 > 65535)
+    return 0;
+  return plan_state8(n_rows, batch * heads, n_keys, head_dim, state8_sms()).ws_bytes;
+}

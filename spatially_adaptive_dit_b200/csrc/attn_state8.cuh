@@ -1,0 +1,124 @@
+// attn_state8.cuh -- what the two kernels of the attention over an 8-bit state
+// share: the call's parameters, the widening of codes, the masks' arithmetic
+// and the record of a part of the keys.
+//
+//   K = k8 * ks, V = v8 * vs (one scale for each block of keys and head)
+//   t_j = (scale log2 e) ks q . k8_j + pad_j log2 e,   p_j = 2^t_j
+//   out = sum_j p_j vs_j v8_j / sum_j p_j
+//
+// Scales never touch a code: ks goes into the score's factor, and vs into the
+// exponent of the weight w_j = 2^(t_j + log2 vs_j - m), m the running maximum
+// of t_j + log2 vs_j.  So the weights that the tensor cores multiply with the
+// codes are at most 2^8 (with the lazy rescale) whatever the scales' range,
+// and f16 holds them to 2^-12; the row sum is sum_j w_j / vs_j in fp32.  Codes
+// of both types are exact in f16, as is a bf16 query row after a power of two
+// has brought its largest element to 2^12 (elements 2^-29 below it lose bits:
+// 2^-36 of the row's largest), so the f16 weights are the only rounding.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace sd {
+
+struct State8Params {
+  const __nv_bfloat16* q;
+  int64_t q_sb, q_sh, q_sr;
+  const uint8_t *k, *v;
+  int64_t k_sb, k_sh, k_sr, v_sb, v_sh, v_sr;
+  const float *ks, *vs;
+  int64_t ks_sb, ks_sh, vs_sb, vs_sh;
+  int block_log2;
+  const int* idx;  // nullable
+  int n_rows, Nq, Nk, H;
+  float scale_log2;  // softmax scale * log2(e)
+  const float* pad;  // nullable, [B, Nk]
+  int64_t pad_sb;
+  __nv_bfloat16* out;
+  int64_t o_sb, o_sh, o_sr;
+  int out_scattered;
+  int* status;
+  uint64_t wait_limit;
+  // Parts of the keys: records of `tile_rows` query rows each, see PartView.
+  int n_split, tile_rows, n_tiles;
+  float* part;
+  int64_t n_records;
+};
+
+constexpr float kLog2eF = 1.4426950408889634f;
+constexpr float kScaleSpread = 64.f;  // log2 of the widest spread of V scales in one slice
+
+// pad in log2 units; a finite pad stays finite, so a row whose keys all carry
+// the type's lowest value averages them instead of being empty.
+__device__ __forceinline__ float pad_log2(float pad) {
+  const float v = pad * kLog2eF;
+  return (fabsf(v) == INFINITY && fabsf(pad) != INFINITY) ? copysignf(3.0e38f, v) : v;
+}
+
+// Two codes in the low half of `w` -> f16x2, exact.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
+  uint32_t r;
+  if constexpr (E4M3) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  } else {  // bytes biased by 128: 0x6400 | u is 1024 + u in f16
+    const uint32_t m = __byte_perm(w, 0x64646464u, 0x4140);
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x64806480u));
+  }
+  return r;
+}
+template <bool E4M3>
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
+  uint32_t r;
+  if constexpr (E4M3) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  } else {
+    const uint32_t m = __byte_perm(w, 0x64646464u, 0x4342);
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x64806480u));
+  }
+  return r;
+}
+// What the widening expects: int8 codes biased to 0..255, e4m3 as they are.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t bias_codes(uint32_t w) {
+  return E4M3 ? w : w ^ 0x80808080u;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Factor 2^f that brings a row's largest magnitude (its fp32 bits) to
+// [2^12, 2^13), and its inverse times `scale`.
+__device__ __forceinline__ float query_factor(uint32_t max_bits, float scale, float& undo) {
+  int e = int(max_bits >> 23) - 127;
+  if (max_bits == 0u) e = 12;  // a zero row
+  int f = 12 - e;
+  f = f > 126 ? 126 : f;
+  undo = scale * __uint_as_float(uint32_t(127 - f) << 23);
+  return __uint_as_float(uint32_t(127 + f) << 23);
+}
+
+// A part's record: O [rows][D] unnormalised, (m, l) [rows], and the smallest
+// and largest log2 vs that it met (of all records behind one another).
+struct PartView {
+  float* o;
+  float* ml;
+  float* range;
+};
+__host__ __device__ inline size_t part_floats(int64_t records, int rows, int D) {
+  return size_t(records) * (size_t(rows) * (D + 2) + 2);
+}
+__device__ __forceinline__ PartView part_view(const State8Params& p, int64_t rec, int D) {
+  PartView v;
+  v.o = p.part + rec * p.tile_rows * D;
+  v.ml = p.part + p.n_records * p.tile_rows * D + rec * p.tile_rows * 2;
+  v.range = p.part + p.n_records * p.tile_rows * (D + 2) + rec * 2;
+  return v;
+}
+
+}  // namespace sd

@@ -1,0 +1,324 @@
+// state8.cu -- rows written into the 8-bit state.
+//
+//   scale = max |x| / qmax over the block's rows and the head's width,
+//   code  = x qmax / max |x|, rounded once to the nearest code (ties to even),
+//
+// with the rows rotated in fp32 first where the tensor asks for it (K before
+// its rounding to 8 bits, so no 16-bit rounding comes between).  Bound by
+// memory: 3 bytes for each 16-bit element.  One CTA holds one block of tokens
+// in registers, reads it once, and walks the heads of its group with the
+// angles of its tokens kept, the next head's loads in flight while this one
+// is reduced (one barrier for each head).
+#include <type_traits>
+
+#include <cuda_fp16.h>
+
+#include "rope.cuh"
+#include "state8.cuh"
+
+namespace sd {
+
+constexpr int kMaxStoreTensors = 4;
+// a block whose magnitudes all lie below this is scaled as if its largest were this
+constexpr float kLeastMax = 7.888609052210118e-31f;  // 2^-100
+
+struct StoreParams {
+  RopeTable tab;
+  RopePos pos;
+  const void* src[kMaxStoreTensors];
+  uint8_t* code[kMaxStoreTensors];
+  float* scale[kMaxStoreTensors];
+  int64_t s_sb[kMaxStoreTensors], s_sh[kMaxStoreTensors], s_sr[kMaxStoreTensors];
+  int64_t c_sb[kMaxStoreTensors], c_sh[kMaxStoreTensors], c_sr[kMaxStoreTensors];
+  int64_t f_sb[kMaxStoreTensors], f_sh[kMaxStoreTensors];
+  int rotate[kMaxStoreTensors];
+  int head_end[kMaxStoreTensors];
+  int n_heads, heads_per_group, any_rotate, slots, e4m3;
+  int n_rows, row0, state_rows;
+  int64_t limit;
+  const int* idx;
+  int src_indexed;
+  int* status;
+};
+
+// Four fp32 values already scaled into the code's range -> four codes.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
+  if constexpr (E4M3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return uint32_t(lo) | uint32_t(hi) << 16;
+  } else {
+    // adding 1.5 * 2^23 rounds to an integer (ties to even) in the low bits
+    constexpr float kMagic = 12582912.f;
+    const uint32_t w0 = __float_as_uint(a + kMagic), w1 = __float_as_uint(b + kMagic);
+    const uint32_t w2 = __float_as_uint(c + kMagic), w3 = __float_as_uint(d + kMagic);
+    return __byte_perm(__byte_perm(w0, w1, 0x0040), __byte_perm(w2, w3, 0x0040), 0x5410);
+  }
+}
+
+// BLOCK tokens, RP rows side by side (thread = slot of a row, d / 8 slots),
+// R = BLOCK / RP rows of each thread.
+template <int BLOCK>
+struct StoreCfg {
+  static constexpr int RP = BLOCK <= 32 ? 16 : 32;
+  static constexpr int R = BLOCK / RP;
+  static constexpr int MAX_THREADS = RP * 16;
+};
+
+template <typename T, int BLOCK, bool HALVES>
+__global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS)
+    state8_store_kernel(const __grid_constant__ StoreParams p) {
+  using C = StoreCfg<BLOCK>;
+  constexpr int NW = SlotWords<T>::N;
+  const float qmax = p.e4m3 ? 448.f : 127.f;
+  __shared__ uint32_t part[2][C::MAX_THREADS / 32];
+  const int rr = threadIdx.x / p.slots, slot = threadIdx.x - rr * p.slots;
+  const int lane = threadIdx.x & 31, warps = int(blockDim.x) >> 5;
+  const int b = blockIdx.z;
+  const int r0 = blockIdx.x * BLOCK;
+  int lo = slot * 8, hi = slot * 8 + 4;
+  if (HALVES && p.any_rotate) lo = p.tab.lo[slot], hi = p.tab.hi[slot];
+  int64_t from[C::R];  // source row, -1: none (its codes are zero)
+  float c[C::R][4], s[C::R][4];
+#pragma unroll
+  for (int k = 0; k < C::R; ++k) {
+    const int r = r0 + rr + k * C::RP;
+    from[k] = -1;
+    int64_t i = r;
+    if (r < p.n_rows) {
+      from[k] = r;
+      if (p.idx) {
+        i = __ldg(p.idx + r);
+        const bool in = i >= 0 && i < p.limit;
+        if (!in) set_status(p.status, SAFEDIT_ERR_INDEX);
+        from[k] = !in ? -1 : p.src_indexed ? i : r;
+      }
+    }
+    if (p.any_rotate) {
+      if (from[k] >= 0) {
+        rope_angles(p.tab, p.pos, b, i, slot, 1.f, c[k], s[k]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[k][j] = 1.f, s[k][j] = 0.f;
+      }
+    }
+  }
+  const int h_begin = blockIdx.y * p.heads_per_group;
+  const int h_end = min(p.n_heads, h_begin + p.heads_per_group);
+  uint32_t w[C::R][NW];
+  auto tensor_of = [&](int hh, int& t, int& h) {
+    t = 0;
+    while (hh >= p.head_end[t]) ++t;
+    h = t ? hh - p.head_end[t - 1] : hh;
+  };
+  auto load = [&](int hh) {
+    int t, h;
+    tensor_of(hh, t, h);
+    const T* base = static_cast<const T*>(p.src[t]) + b * p.s_sb[t] + h * p.s_sh[t];
+#pragma unroll
+    for (int k = 0; k < C::R; ++k) {
+#pragma unroll
+      for (int e = 0; e < NW; ++e) w[k][e] = 0u;
+      if (from[k] >= 0) slot_load<T, HALVES>(w[k], base + from[k] * p.s_sr[t], lo, hi);
+    }
+  };
+  load(h_begin);
+  for (int hh = h_begin; hh < h_end; ++hh) {
+    int t, h;
+    tensor_of(hh, t, h);
+    float x[C::R][8];
+#pragma unroll
+    for (int k = 0; k < C::R; ++k) slot_widen<T>(w[k], x[k]);
+    if (hh + 1 < h_end) load(hh + 1);
+    if (p.rotate[t]) {
+#pragma unroll
+      for (int k = 0; k < C::R; ++k) rope_turn<HALVES>(x[k], c[k], s[k]);
+    }
+    // largest magnitude of the block: the bits of |x| order as integers, and
+    // infinities and NaN come out on top
+    auto block_max = [&](bool finite_only, int buf) {
+      uint32_t m = 0u;
+#pragma unroll
+      for (int k = 0; k < C::R; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t a = __float_as_uint(x[k][e]) & 0x7FFFFFFFu;
+          m = max(m, finite_only && a >= 0x7F800000u ? 0u : a);
+        }
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (lane == 0) part[buf][threadIdx.x >> 5] = m;
+      __syncthreads();
+      return __reduce_max_sync(0xffffffffu, lane < warps ? part[buf][lane] : 0u);
+    };
+    const int buf = (hh - h_begin) & 1;
+    uint32_t top = block_max(false, buf);
+    if (top >= 0x7F800000u) {  // infinities saturate, NaN becomes 0; reported
+      __syncthreads();
+      top = block_max(true, buf);
+      if (threadIdx.x == 0) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
+      const float big = top ? __uint_as_float(top) : qmax;
+#pragma unroll
+      for (int k = 0; k < C::R; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = x[k][e];
+          if (v != v)
+            x[k][e] = 0.f;
+          else if (fabsf(v) > big)
+            x[k][e] = copysignf(big, v);
+        }
+    }
+    const float most = top ? fmaxf(__uint_as_float(top), kLeastMax) : qmax;
+    if (threadIdx.x == 0)
+      p.scale[t][b * p.f_sb[t] + h * p.f_sh[t] + p.row0 / BLOCK + blockIdx.x] = most / qmax;
+    // x qmax / most with one rounding: both sides by the power of two that
+    // brings `most` into [1, 2) (exact), then Markstein's correction of
+    // x * RN(1 / most).  With 16-bit rows the product x qmax is exact, so a
+    // tie between two codes is met as one; x * (qmax / most) missed ties and
+    // gave the neighbour.
+    const int ex = (int(__float_as_uint(most) >> 23) & 255) - 127;
+    const float m1 = __uint_as_float((__float_as_uint(most) & 0x007FFFFFu) | 0x3F800000u);
+    const float up = __uint_as_float(uint32_t(127 + 6 - ex) << 23) * (qmax / 64.f);  // qmax 2^-ex, exact
+    const float inv = 1.f / m1;
+    uint8_t* crow = p.code[t] + b * p.c_sb[t] + h * p.c_sh[t];
+#pragma unroll
+    for (int k = 0; k < C::R; ++k) {
+      const int dst = p.row0 + r0 + rr + k * C::RP;
+      if (dst >= p.state_rows) continue;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = x[k][e] * up;
+        const float q = a * inv;
+        y[e] = fmaf(fmaf(-q, m1, a), inv, q);
+      }
+      uint32_t o0, o1;
+      if (p.e4m3) {
+        o0 = pack_codes<true>(y[0], y[1], y[2], y[3]);
+        o1 = pack_codes<true>(y[4], y[5], y[6], y[7]);
+      } else {
+        o0 = pack_codes<false>(y[0], y[1], y[2], y[3]);
+        o1 = pack_codes<false>(y[4], y[5], y[6], y[7]);
+      }
+      uint8_t* row = crow + int64_t(dst) * p.c_sr[t];
+      if constexpr (HALVES) {
+        *reinterpret_cast<uint32_t*>(row + lo) = o0;
+        *reinterpret_cast<uint32_t*>(row + hi) = o1;
+      } else {
+        *reinterpret_cast<uint2*>(row + lo) = make_uint2(o0, o1);
+      }
+    }
+  }
+}
+
+template <typename T, int BLOCK, bool HALVES>
+static safedit_status launch_store(StoreParams& p, int64_t B, cudaStream_t s) {
+  const int threads = StoreCfg<BLOCK>::RP * p.slots;
+  const int64_t blocks = (int64_t(p.n_rows) + BLOCK - 1) / BLOCK;
+  // as few head groups as still give every SM 2048 threads twice over
+  const int64_t ctas = 148 * 2 * (2048 / threads);
+  int64_t groups = (ctas + blocks * B - 1) / (blocks * B);
+  if (groups > p.n_heads) groups = p.n_heads;
+  p.heads_per_group = int((p.n_heads + groups - 1) / groups);
+  groups = (p.n_heads + p.heads_per_group - 1) / p.heads_per_group;
+  if (groups > 65535) return SAFEDIT_ERR_UNSUPPORTED;
+  state8_store_kernel<T, BLOCK, HALVES>
+      <<<dim3(unsigned(blocks), unsigned(groups), unsigned(B)), threads, 0, s>>>(p);
+  return after_launch(1);
+}
+
+template <typename T, bool HALVES>
+static safedit_status store_by_block(StoreParams& p, int64_t B, int block, cudaStream_t s) {
+  switch (block) {
+    case 16: return launch_store<T, 16, HALVES>(p, B, s);
+    case 32: return launch_store<T, 32, HALVES>(p, B, s);
+    case 64: return launch_store<T, 64, HALVES>(p, B, s);
+    default: return launch_store<T, 128, HALVES>(p, B, s);
+  }
+}
+
+template <typename T>
+static safedit_status store_by_form(StoreParams& p, int64_t B, int block, bool halves, cudaStream_t s) {
+  return halves ? store_by_block<T, true>(p, B, block, s) : store_by_block<T, false>(p, B, block, s);
+}
+
+}  // namespace sd
+
+using namespace sd;
+
+extern "C" safedit_status safedit_state8_store(const safedit_tensor* src, const safedit_tensor* codes,
+                                               const safedit_tensor* scales, int32_t n_tensors, int32_t block,
+                                               int64_t row0, const int32_t* d_idx, int32_t n_idx,
+                                               int32_t src_indexed, const int32_t* host_rotate,
+                                               const safedit_tensor* pos, const safedit_rope* rope, void* stream) {
+  if (!src || !codes || !scales || n_tensors < 1 || n_tensors > kMaxStoreTensors) return SAFEDIT_ERR_INVALID_ARG;
+  if ((src_indexed != 0 && src_indexed != 1) || row0 < 0) return SAFEDIT_ERR_INVALID_ARG;
+  if (d_idx ? n_idx < 0 : src_indexed) return SAFEDIT_ERR_INVALID_ARG;
+  if (!state8_block_ok(block)) return SAFEDIT_ERR_UNSUPPORTED;
+  if (row0 % block != 0) return SAFEDIT_ERR_ALIGNMENT;
+  StoreParams p{};
+  safedit_status st;
+  int64_t B = -1, d = -1, n = -1, N = -1, heads = 0;
+  for (int t = 0; t < n_tensors; ++t) {
+    const safedit_tensor &x = src[t], &c = codes[t], &f = scales[t];
+    if ((st = check_tensor(&x, 4)) != SAFEDIT_OK) return st;
+    if ((st = check_codes(&c)) != SAFEDIT_OK) return st;
+    if ((st = check_scales(&f, &c, block)) != SAFEDIT_OK) return st;
+    if (x.dtype != SAFEDIT_BF16 && x.dtype != SAFEDIT_F16 && x.dtype != SAFEDIT_F32) return SAFEDIT_ERR_DTYPE;
+    if (x.dtype != src[0].dtype || c.dtype != codes[0].dtype) return SAFEDIT_ERR_DTYPE;
+    if (t == 0) B = x.dims[0], d = x.dims[3], n = d_idx ? int64_t(n_idx) : x.dims[2], N = c.dims[2];
+    if (x.dims[0] != B || c.dims[0] != B || x.dims[3] != d || c.dims[3] != d || c.dims[1] != x.dims[1] ||
+        c.dims[2] != N || (!src_indexed && x.dims[2] != n))
+      return SAFEDIT_ERR_SHAPE;
+    const int64_t vec = 16 / elt_size(x.dtype);
+    if (x.strides[3] != 1 || !aligned16(x.data)) return SAFEDIT_ERR_ALIGNMENT;
+    for (int k = 0; k < 3; ++k)
+      if (x.strides[k] % vec != 0 || x.strides[k] < 0) return SAFEDIT_ERR_ALIGNMENT;
+    heads += x.dims[1];
+    if (heads > INT32_MAX / 2) return SAFEDIT_ERR_SHAPE;
+    p.src[t] = x.data;
+    p.code[t] = static_cast<uint8_t*>(c.data);
+    p.scale[t] = static_cast<float*>(f.data);
+    p.s_sb[t] = x.strides[0], p.s_sh[t] = x.strides[1], p.s_sr[t] = x.strides[2];
+    p.c_sb[t] = c.strides[0], p.c_sh[t] = c.strides[1], p.c_sr[t] = c.strides[2];
+    p.f_sb[t] = f.strides[0], p.f_sh[t] = f.strides[1];
+    p.head_end[t] = int(heads);
+    p.rotate[t] = host_rotate ? host_rotate[t] : 0;
+    if (p.rotate[t] != 0 && p.rotate[t] != 1) return SAFEDIT_ERR_INVALID_ARG;
+    p.any_rotate |= p.rotate[t];
+  }
+  if (d != 64 && d != 96 && d != 128) return SAFEDIT_ERR_UNSUPPORTED;
+  if (row0 > N || n > N - row0 || N > INT32_MAX - 128) return SAFEDIT_ERR_SHAPE;
+  if (B > 65535) return SAFEDIT_ERR_UNSUPPORTED;
+  p.limit = INT32_MAX;
+  if (p.any_rotate) {
+    int64_t tokens = 0;
+    if ((st = rope_setup(rope, pos, B, d, &p.tab, &p.pos, &tokens)) != SAFEDIT_OK) return st;
+    if (rope->inverse) return SAFEDIT_ERR_INVALID_ARG;
+    if (!d_idx && tokens < n) return SAFEDIT_ERR_SHAPE;
+    p.limit = tokens;
+  }
+  if (src_indexed)
+    for (int t = 0; t < n_tensors; ++t)
+      if (src[t].dims[2] < p.limit) p.limit = src[t].dims[2];
+  if (n == 0 || B == 0 || heads == 0) return SAFEDIT_OK;
+  p.n_heads = int(heads);
+  p.slots = int(d / 8);
+  p.e4m3 = codes[0].dtype == SAFEDIT_E4M3;
+  p.n_rows = int(n);
+  p.row0 = int(row0);
+  p.state_rows = int(N);
+  p.idx = d_idx;
+  p.src_indexed = src_indexed;
+  p.status = status_ptr();
+  if (!p.status) return SAFEDIT_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool halves = p.any_rotate && rope->halves;
+  switch (src[0].dtype) {
+    case SAFEDIT_BF16: return store_by_form<__nv_bfloat16>(p, B, block, halves, s);
+    case SAFEDIT_F16: return store_by_form<__half>(p, B, block, halves, s);
+    default: return store_by_form<float>(p, B, block, halves, s);
+  }
+}

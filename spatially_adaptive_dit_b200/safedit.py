@@ -8,6 +8,7 @@ has not been built: there is no CPU fallback.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -24,15 +25,18 @@ _lib = ctypes.CDLL(LIB_PATH)
 # ---- enums (mirror include/safedit.h) -------------------------------------
 OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_DTYPE, ERR_ALIGNMENT, ERR_INDEX, ERR_UNSUPPORTED, ERR_CUDA, \
     ERR_TIMEOUT, ERR_MASKED_ROW = range(10)
-F32, BF16, F16, BOOL, I32, F64, U8 = range(7)
+F32, BF16, F16, BOOL, I32, F64, U8, I8, E4M3 = range(9)
+ROPE_INTERLEAVED, ROPE_HALVES = 0, 1
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.bool: BOOL,
-          torch.int32: I32, torch.float64: F64, torch.uint8: U8}
+          torch.int32: I32, torch.float64: F64, torch.uint8: U8, torch.int8: I8, torch.float8_e4m3fn: E4M3}
 
 EXPORTED = ("safedit_cross_attn_probs", "safedit_partition_accumulate", "safedit_pcsp_score",
             "safedit_partition_finalize", "safedit_mask_is_row_constant", "safedit_attn_subset",
             "safedit_attn_subset_ws", "safedit_attn_subset_workspace_size", "safedit_attn_subset_noalloc",
             "safedit_scatter_state", "safedit_gather_rows", "safedit_sw_cfg", "safedit_stepcache_sw_cfg",
+            "safedit_rope_rows", "safedit_state8_store", "safedit_attn_subset_state8",
+            "safedit_attn_subset_state8_workspace_size",
             "safedit_gemm_bias_act", "safedit_get_device_status", "safedit_status_string", "safedit_kernel_launch_count",
             "safedit_debug_set_wait_limit_ns", "safedit_debug_set_index_check")
 
@@ -40,6 +44,11 @@ EXPORTED = ("safedit_cross_attn_probs", "safedit_partition_accumulate", "safedit
 class SafeditTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("ndim", ctypes.c_int32),
                 ("dims", ctypes.c_int64 * 4), ("strides", ctypes.c_int64 * 4)]
+
+
+class SafeditRope(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("halves", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("axis_dim", ctypes.c_int32 * 4), ("theta", ctypes.c_double * 4)]
 
 
 class SafeditError(RuntimeError):
@@ -69,6 +78,15 @@ _lib.safedit_gather_rows.argtypes = [_T, _T, _i32, _vp, _i32, _vp]
 _lib.safedit_sw_cfg.argtypes = [_T, _T, _vp, _f32, _f32, _T, _vp]
 _lib.safedit_stepcache_sw_cfg.argtypes = [_T, _T, _T, _T, _vp, _f32, _f32, _f32, _T, _vp]
 _lib.safedit_gemm_bias_act.argtypes = [_T, _T, _vp, _i32, _vp, _T, _vp]
+_R = ctypes.POINTER(SafeditRope)
+# the descriptors of the calls below travel as packed bytes (see _packed)
+_lib.safedit_rope_rows.argtypes = [_vp, _vp, _i32, _vp, _R, _vp, _i32, _i32, _i32, _vp]
+_lib.safedit_state8_store.argtypes = [_vp, _vp, _vp, _i32, _i32, ctypes.c_int64, _vp, _i32, _i32, _vp, _vp, _R, _vp]
+_lib.safedit_attn_subset_state8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _f32, _vp, _i32, _vp,
+                                            ctypes.c_size_t, _vp]
+_lib.safedit_attn_subset_state8_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                           ctypes.c_int64, _i32]
+_lib.safedit_attn_subset_state8_workspace_size.restype = ctypes.c_size_t
 _lib.safedit_get_device_status.argtypes = [ctypes.POINTER(ctypes.c_int32), _vp]
 _lib.safedit_status_string.argtypes = [ctypes.c_int]
 _lib.safedit_status_string.restype = ctypes.c_char_p
@@ -80,7 +98,7 @@ _lib.safedit_debug_set_index_check.restype = ctypes.c_int32
 for _n in EXPORTED:
     if _n not in ("safedit_status_string", "safedit_kernel_launch_count",
                   "safedit_debug_set_wait_limit_ns", "safedit_debug_set_index_check",
-                  "safedit_attn_subset_workspace_size"):
+                  "safedit_attn_subset_workspace_size", "safedit_attn_subset_state8_workspace_size"):
         getattr(_lib, _n).restype = ctypes.c_int
 
 
@@ -230,6 +248,102 @@ def safedit_gemm_bias_act(a, w, bias, act, idx_out, out, stream=None):
     _check(_lib.safedit_gemm_bias_act(_ref(a), _ref(w), _ptr(bias), int(act), _ptr(idx_out), _ref(out),
                                       _stream(stream)),
            "safedit_gemm_bias_act")
+
+
+# safedit_tensor as packed bytes: a third of the time of filling the ctypes
+# structure, which is most of a small call's
+_TENSOR = struct.Struct("Pii8q")
+_TENSOR3 = struct.Struct("Pii3q8x3q8x")
+assert _TENSOR.size == _TENSOR3.size == ctypes.sizeof(SafeditTensor)
+
+
+def _packed(t, device):
+    """`t` as the bytes of a safedit_tensor; it has to live on the current device (number `device`)."""
+    if t.get_device() != device:
+        raise SafeditError(ERR_INVALID_ARG, f"a tensor on {t.device}, with cuda:{device} the current device")
+    if t.dtype not in _DTYPE:
+        raise SafeditError(ERR_DTYPE, f"a tensor of {t.dtype}")
+    n = t.dim()
+    if n == 4:
+        return _TENSOR.pack(t.data_ptr(), _DTYPE[t.dtype], 4, *t.shape, *t.stride())
+    if n == 3:
+        return _TENSOR3.pack(t.data_ptr(), _DTYPE[t.dtype], 3, *t.shape, *t.stride())
+    if n < 1 or n > 4:
+        raise SafeditError(ERR_SHAPE, "a tensor of 1 to 4 dims is wanted")
+    pad = (0,) * (4 - n)
+    return _TENSOR.pack(t.data_ptr(), _DTYPE[t.dtype], n, *t.shape, *pad, *t.stride(), *pad)
+
+
+def _packed_all(ts, device):
+    return b"".join([_packed(t, device) for t in ts])
+
+
+def _index_arg(idx, n_idx, device):
+    """A row index: int32, contiguous, on the current device, at least n_idx entries; None stays NULL."""
+    if idx is None:
+        return None
+    if idx.dtype != torch.int32:
+        raise SafeditError(ERR_DTYPE, f"an index of {idx.dtype}")
+    if idx.get_device() != device or not idx.is_contiguous() or idx.numel() < n_idx:
+        raise SafeditError(ERR_INVALID_ARG, "an index: contiguous, on the current device, with n_idx entries")
+    return _idx_ptr(idx)
+
+
+def rope_spec(axis_dims, thetas, layout=ROPE_INTERLEAVED, inverse=False) -> SafeditRope:
+    """Segment widths and frequency bases of 1 to 4 axes; layout: ROPE_INTERLEAVED or ROPE_HALVES."""
+    if len(axis_dims) != len(thetas) or not 1 <= len(axis_dims) <= 4:
+        raise SafeditError(ERR_INVALID_ARG, "rope_spec: one to four axes, each with a base")
+    r = SafeditRope()
+    r.n_axes, r.halves, r.inverse = len(axis_dims), int(layout), int(bool(inverse))
+    r.axis_dim[:len(axis_dims)] = [int(a) for a in axis_dims]
+    r.theta[:len(thetas)] = [float(t) for t in thetas]
+    return r
+
+
+def safedit_rope_rows(src, dst, pos, rope, idx=None, n_idx=0, src_indexed=False, dst_indexed=False, stream=None):
+    """src, dst: sequences of tensors (same length, 1..4); rope: rope_spec(...)."""
+    dev = torch.cuda.current_device()
+    if len(src) != len(dst):
+        raise SafeditError(ERR_INVALID_ARG, "safedit_rope_rows: as many dst as src")
+    _check(_lib.safedit_rope_rows(_packed_all(src, dev), _packed_all(dst, dev), len(src), _packed(pos, dev), rope,
+                                  _index_arg(idx, n_idx, dev), int(n_idx), int(src_indexed), int(dst_indexed),
+                                  _stream(stream)), "safedit_rope_rows")
+
+
+def safedit_state8_store(src, codes, scales, block, row0=0, idx=None, n_idx=0, src_indexed=False, rotate=None,
+                         pos=None, rope=None, stream=None):
+    """src, codes, scales: sequences of tensors (same length, 1..4); rotate: which of
+    them are rotated at pos by rope_spec(...) first, or None."""
+    dev = torch.cuda.current_device()
+    if len(codes) != len(src) or len(scales) != len(src) or (rotate is not None and len(rotate) != len(src)):
+        raise SafeditError(ERR_INVALID_ARG, "safedit_state8_store: as many codes, scales and flags as src")
+    flags = None if rotate is None else struct.pack("%di" % len(src), *map(bool, rotate))
+    _check(_lib.safedit_state8_store(_packed_all(src, dev), _packed_all(codes, dev), _packed_all(scales, dev), len(src),
+                                     int(block), int(row0), _index_arg(idx, n_idx, dev), int(n_idx), int(src_indexed),
+                                     flags, None if pos is None else _packed(pos, dev), rope, _stream(stream)),
+           "safedit_state8_store")
+
+
+def safedit_attn_subset_state8(q, k8, k_scale, v8, v_scale, block, idx, n_idx, key_pad, scale, out, out_scattered,
+                               workspace=None, stream=None):
+    """workspace: a device tensor of at least safedit_attn_subset_state8_workspace_size(...)
+    bytes, or None when that size is 0."""
+    dev = torch.cuda.current_device()
+    ptr = nbytes = 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise SafeditError(ERR_INVALID_ARG, "a workspace: contiguous, on the current device")
+        ptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(_lib.safedit_attn_subset_state8(_packed(q, dev), _packed(k8, dev), _packed(k_scale, dev), _packed(v8, dev),
+                                           _packed(v_scale, dev), int(block), _index_arg(idx, n_idx, dev), int(n_idx),
+                                           None if key_pad is None else _packed(key_pad, dev), float(scale),
+                                           _packed(out, dev), int(out_scattered), ptr, nbytes, _stream(stream)),
+           "safedit_attn_subset_state8")
+
+
+def safedit_attn_subset_state8_workspace_size(batch, heads, n_rows, n_keys, head_dim) -> int:
+    return int(_lib.safedit_attn_subset_state8_workspace_size(int(batch), int(heads), int(n_rows), int(n_keys),
+                                                              int(head_dim)))
 
 
 def safedit_get_device_status(stream=None) -> int:
