@@ -297,10 +297,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) attn_state8_rows_kernel(const 
   const int64_t rec = (int64_t(bh) * p.n_tiles + tile) * p.n_split + split;
   if (p.n_split > 1) {
     const PartView pv = part_view(p, rec, D);
-    for (int e = threadIdx.x; e < 16 * D; e += kRowWarps * 32) pv.o[e] = (&sm_o[0][0])[e];
+    for (int e = threadIdx.x; e < p.tile_rows * D; e += kRowWarps * 32) pv.o[e] = (&sm_o[0][0])[e];
     if (warp == 0 && t == 0) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) pv.ml[(g + 8 * r) * 2] = mx[r], pv.ml[(g + 8 * r) * 2 + 1] = lx[r];
+      for (int r = 0; r < 2; ++r)
+        if (g + 8 * r < p.tile_rows) pv.ml[(g + 8 * r) * 2] = mx[r], pv.ml[(g + 8 * r) * 2 + 1] = lx[r];
     }
     if (threadIdx.x == 0) pv.range[0] = lv_lo, pv.range[1] = lv_hi;
     return;
@@ -330,12 +331,15 @@ __global__ void __launch_bounds__(kRowWarps * 32) attn_state8_rows_kernel(const 
 template <int D>
 __global__ void __launch_bounds__(D) attn_state8_join_kernel(const __grid_constant__ State8Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int r = blockIdx.x, bh = blockIdx.y, c = threadIdx.x;
+  const int c = threadIdx.x;
+  const int pu = blockIdx.x / p.tile_rows, rr = blockIdx.x - pu * p.tile_rows;
+  const int unit = p.n_full + pu;
+  const int bh = unit / p.n_tiles, r = (unit - bh * p.n_tiles) * p.unit_rows + rr;
+  if (r >= p.n_rows) return;
   const int b = bh / p.H, h = bh - b * p.H;
-  const int tile = r / p.tile_rows, rr = r - tile * p.tile_rows;
   const int qi = p.idx ? __ldg(p.idx + r) : r;
   if (qi < 0 || qi >= p.Nq) return;  // reported by the attention kernel
-  const int64_t rec0 = (int64_t(bh) * p.n_tiles + tile) * p.n_split;
+  const int64_t rec0 = int64_t(pu) * p.n_split;
   float m = -INFINITY, lv_lo = INFINITY, lv_hi = -INFINITY;
   for (int s = 0; s < p.n_split; ++s) {
     const PartView v = part_view(p, rec0 + s, D);
@@ -361,8 +365,9 @@ __global__ void __launch_bounds__(D) attn_state8_join_kernel(const __grid_consta
 
 // ------------------------------------------------------------- plan
 struct State8Plan {
-  int tile_rows = 16, n_tiles = 0, n_split = 1;
-  int64_t n_records = 0;
+  bool tc = false;
+  int unit_rows = 16, tile_rows = 16, n_tiles = 0, n_full = 0, n_split = 1;
+  int64_t n_parts = 0;  // units that run in parts
   size_t ws_bytes = 0;
 };
 
@@ -374,27 +379,51 @@ static int state8_sms() {
   return sms;
 }
 
+// Rows of a slice up to which the warp-level kernel is taken.
+constexpr int64_t kFewRows = 16;
+
 static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int sms) {
   State8Plan pl;
-  pl.n_tiles = int((n_rows + 15) / 16);
-  const int64_t ctas = pl.n_tiles * BH;
-  // three CTAs on an SM, each warp at least two groups of 16 keys
-  int64_t split = ctas > 0 ? int64_t(sms) * 3 / ctas : 1;
-  const int64_t most = (Nk + 16 * kRowWarps * 2 - 1) / (16 * kRowWarps * 2);
-  if (split > most) split = most;
-  if (split < 1) split = 1;
-  pl.n_split = int(split);
-  if (split > 1) {
-    pl.n_records = ctas * split;
-    pl.ws_bytes = part_floats(pl.n_records, pl.tile_rows, D) * sizeof(float);
+  pl.tc = n_rows > kFewRows;
+  pl.unit_rows = pl.tc ? 256 : 16;
+  pl.tile_rows = n_rows < pl.unit_rows ? int(n_rows) : pl.unit_rows;
+  pl.n_tiles = int((n_rows + pl.unit_rows - 1) / pl.unit_rows);
+  const int64_t units = pl.n_tiles * BH;
+  if (units == 0) return pl;
+  if (!pl.tc) {
+    // three CTAs on an SM, each warp at least two groups of 16 keys
+    int64_t split = int64_t(sms) * 3 / units;
+    const int64_t most = (Nk + 16 * kRowWarps * 2 - 1) / (16 * kRowWarps * 2);
+    if (split > most) split = most;
+    pl.n_split = split > 1 ? int(split) : 1;
+    pl.n_parts = split > 1 ? units : 0;
+  } else {
+    // The units that do not fill a wave of the SMs run as 2..16 parts over
+    // the key tiles where that ends the call sooner: a CTA costs about
+    // kFixedUs and kTileUs a key tile of 128, the join kJoinUs.
+    constexpr double kFixedUs = 9.0, kTileUs = 1.9, kJoinUs = 5.0;
+    const int64_t nk = (Nk + 127) / 128, tail = units % sms;
+    const double tile_us = kTileUs * (D + 32) / 128.0;
+    double best = kFixedUs + double(nk) * tile_us;
+    for (int s = 2; tail > 0 && s <= 16 && s <= nk; ++s) {
+      const double rounds = double((tail * s + sms - 1) / sms);
+      const double cost = rounds * (kFixedUs + double((nk + s - 1) / s) * tile_us) + kJoinUs;
+      if (cost < best) {
+        best = cost;
+        pl.n_split = s;
+      }
+    }
+    pl.n_parts = pl.n_split > 1 ? tail : 0;
   }
+  pl.n_full = int(units - pl.n_parts);
+  if (pl.n_parts) pl.ws_bytes = part_floats(pl.n_parts * pl.n_split, pl.tile_rows, D) * sizeof(float);
   return pl;
 }
 
 template <int D>
-static safedit_status launch_join(const State8Params& p, int64_t BH, cudaStream_t s) {
+static safedit_status launch_join(const State8Params& p, int64_t n_parts, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.n_rows), unsigned(BH));
+  cfg.gridDim = dim3(unsigned(n_parts * p.tile_rows));
   cfg.blockDim = dim3(D);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -406,19 +435,28 @@ static safedit_status launch_join(const State8Params& p, int64_t BH, cudaStream_
   return after_launch(1);
 }
 
-template <int D, bool PAD, bool E4M3>
-static safedit_status launch_state8(const State8Params& p, int64_t BH, cudaStream_t s) {
-  attn_state8_rows_kernel<D, PAD, E4M3>
-      <<<dim3(unsigned(p.n_split), unsigned(p.n_tiles), unsigned(BH)), kRowWarps * 32, 0, s>>>(p);
-  safedit_status st = after_launch(1);
-  if (st != SAFEDIT_OK || p.n_split == 1) return st;
-  return launch_join<D>(p, BH, s);
+template <int D, bool PAD>
+static safedit_status launch_rows(const State8Params& p, int64_t BH, bool e4m3, cudaStream_t s) {
+  const dim3 grid{unsigned(p.n_split), unsigned(p.n_tiles), unsigned(BH)};
+  if (e4m3)
+    attn_state8_rows_kernel<D, PAD, true><<<grid, kRowWarps * 32, 0, s>>>(p);
+  else
+    attn_state8_rows_kernel<D, PAD, false><<<grid, kRowWarps * 32, 0, s>>>(p);
+  return after_launch(1);
 }
 
 template <int D>
-static safedit_status dispatch_state8(const State8Params& p, int64_t BH, bool e4m3, cudaStream_t s) {
-  if (p.pad) return e4m3 ? launch_state8<D, true, true>(p, BH, s) : launch_state8<D, true, false>(p, BH, s);
-  return e4m3 ? launch_state8<D, false, true>(p, BH, s) : launch_state8<D, false, false>(p, BH, s);
+static safedit_status dispatch_state8(const safedit_tensor* k8, const safedit_tensor* v8, const State8Params& p,
+                                      const State8Plan& pl, int64_t BH, cudaStream_t s) {
+  safedit_status st;
+  if (pl.tc)
+    st = launch_state8_tc(k8, v8, p, pl.n_full + pl.n_parts * pl.n_split, s);
+  else if (p.pad)
+    st = launch_rows<D, true>(p, BH, k8->dtype == SAFEDIT_E4M3, s);
+  else
+    st = launch_rows<D, false>(p, BH, k8->dtype == SAFEDIT_E4M3, s);
+  if (st != SAFEDIT_OK || pl.n_parts == 0) return st;
+  return launch_join<D>(p, pl.n_parts, s);
 }
 
 static safedit_status check_rows16(const safedit_tensor* t) {
@@ -461,7 +499,7 @@ extern "C" safedit_status safedit_attn_subset_state8(const safedit_tensor* q, co
   const int64_t n_rows = d_idx ? n_idx : Nq;
   if (out->dims[0] != B || out->dims[1] != H || out->dims[3] != D) return SAFEDIT_ERR_SHAPE;
   if (out->dims[2] != (out_scattered ? Nq : n_rows)) return SAFEDIT_ERR_SHAPE;
-  if ((n_rows + 15) / 16 > 65535) return SAFEDIT_ERR_SHAPE;
+  if ((n_rows + 255) / 256 * B * H * 16 > INT32_MAX) return SAFEDIT_ERR_SHAPE;  // parts counted in int
   State8Params p{};
   if (key_pad) {
     if ((st = check_tensor(key_pad, 2)) != SAFEDIT_OK) return st;
@@ -500,10 +538,12 @@ extern "C" safedit_status safedit_attn_subset_state8(const safedit_tensor* q, co
   p.o_sb = out->strides[0], p.o_sh = out->strides[1], p.o_sr = out->strides[2];
   p.out_scattered = out_scattered;
   p.wait_limit = wait_limit_ns();
+  p.n_full = pl.n_full;
   p.n_split = pl.n_split;
+  p.unit_rows = pl.unit_rows;
   p.tile_rows = pl.tile_rows;
   p.n_tiles = pl.n_tiles;
-  p.n_records = pl.n_records;
+  p.n_records = pl.n_parts * pl.n_split;
   p.part = static_cast<float*>(d_workspace);
   p.status = status_ptr();
   if (!p.status) return SAFEDIT_ERR_CUDA;
@@ -511,11 +551,10 @@ extern "C" safedit_status safedit_attn_subset_state8(const safedit_tensor* q, co
   if (d_idx && out_scattered && index_check_enabled() &&
       (st = launch_index_check(d_idx, int32_t(n_rows), Nq, p.status, s)) != SAFEDIT_OK)
     return st;
-  const bool e4m3 = k8->dtype == SAFEDIT_E4M3;
   switch (D) {
-    case 64: return dispatch_state8<64>(p, B * H, e4m3, s);
-    case 96: return dispatch_state8<96>(p, B * H, e4m3, s);
-    default: return dispatch_state8<128>(p, B * H, e4m3, s);
+    case 64: return dispatch_state8<64>(k8, v8, p, pl, B * H, s);
+    case 96: return dispatch_state8<96>(k8, v8, p, pl, B * H, s);
+    default: return dispatch_state8<128>(k8, v8, p, pl, B * H, s);
   }
 }
 
@@ -524,7 +563,7 @@ extern "C" size_t safedit_attn_subset_state8_workspace_size(int64_t batch, int64
   if (batch <= 0 || heads <= 0 || n_rows <= 0 || n_keys <= 0) return 0;
   if (head_dim != 64 && head_dim != 96 && head_dim != 128) return 0;
   if (batch > 65535 || heads > 65535 || batch * heads > 65535 || n_keys > INT32_MAX - 256 ||
-      (n_rows + 15) / 16 > 65535)
+      n_rows > INT32_MAX || (n_rows + 255) / 256 * batch * heads * 16 > INT32_MAX)
     return 0;
   return plan_state8(n_rows, batch * heads, n_keys, head_dim, state8_sms()).ws_bytes;
 }

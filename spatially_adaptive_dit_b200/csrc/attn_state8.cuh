@@ -41,8 +41,10 @@ struct State8Params {
   int out_scattered;
   int* status;
   uint64_t wait_limit;
-  // Parts of the keys: records of `tile_rows` query rows each, see PartView.
-  int n_split, tile_rows, n_tiles;
+  // Schedule: units of query rows (n_tiles of them in a (b, h) slice).  Units
+  // below n_full run whole; each later one as n_split parts over the keys,
+  // whose records (of `tile_rows` rows, see PartView) are joined afterwards.
+  int n_full, n_split, unit_rows, tile_rows, n_tiles;
   float* part;
   int64_t n_records;
 };
@@ -120,5 +122,9 @@ __device__ __forceinline__ PartView part_view(const State8Params& p, int64_t rec
   v.range = p.part + p.n_records * p.tile_rows * (D + 2) + rec * 2;
   return v;
 }
+
+// The tensor-core kernel over `ctas` CTAs (whole units and parts).
+safedit_status launch_state8_tc(const safedit_tensor* k8, const safedit_tensor* v8, const State8Params& p,
+                                int64_t ctas, cudaStream_t s);
 
 }  // namespace sd

@@ -145,9 +145,9 @@ def test_store_refusals(sd):
 
 
 def test_attention_refusals(sd):
-    B, H, Nq, N, D = 1, 2, 100, 300, 64
+    B, H, Nq, N, D = 1, 2, 100, 3000, 64
     q, o = desc(sd, (B, H, Nq, D), sd.BF16), desc(sd, (B, H, Nq, D), sd.BF16)
-    k, f = desc(sd, (B, H, N, D), sd.E4M3), desc(sd, (B, H, 5), sd.F32)
+    k, f = desc(sd, (B, H, N, D), sd.E4M3), desc(sd, (B, H, 47), sd.F32)
     big = 1 << 30
 
     def go(q=q, k=k, ks=f, v=k, vs=f, block=64, idx=None, n_idx=0, pad=None, o=o, scat=0, ws=0x40000, nb=big):
@@ -174,7 +174,7 @@ def test_attention_refusals(sd):
     assert go(pad=desc(sd, (B, N), sd.BF16)) == sd.ERR_DTYPE
     assert go(pad=desc(sd, (B, N + 1), sd.F32)) == sd.ERR_SHAPE
     assert go(pad=desc(sd, (B, N), sd.F32, ptr=0x10004)) == sd.ERR_ALIGNMENT
-    assert go(pad=desc(sd, (B, N), sd.F32, strides=(301, 1))) == sd.ERR_ALIGNMENT
+    assert go(pad=desc(sd, (B, N), sd.F32, strides=(3001, 1))) == sd.ERR_ALIGNMENT
     # the workspace: large enough, aligned, given
     need = sd.safedit_attn_subset_state8_workspace_size(B, H, Nq, N, D)
     assert need > 0
