@@ -1,14 +1,14 @@
 // attn_state8_tc.cu -- attention of many query rows over an 8-bit state, on
 // the fifth-generation tensor cores.
 //
-// One CTA per SM, 512 threads = 4 warpgroups, 256 query rows (two tiles of
-// 128) of one (b, h) slice against a range of the keys:
+// One CTA per SM, 384 threads = 12 warps, 256 query rows (two tiles of 128)
+// of one (b, h) slice against a range of the keys:
 //   * warpgroups 0 and 1: the softmax of one tile each, thread = query row =
 //     TMEM lane.  They first gather their rows, scale them to f16 and lay them
 //     out for the tensor core.
-//   * warpgroup 2: warp 8 streams the codes of K and V by TMA (128 keys a
-//     tile) into a ring; warp 9 issues tcgen05.mma.
-//   * warpgroup 3 widens codes to f16 into the swizzled tiles that the tensor
+//   * warp 11 issues tcgen05.mma.
+//   * warps 8 to 10 stream the codes of K and V by TMA (128 keys a tile) into a
+//     ring and widens codes to f16 into the swizzled tiles that the tensor
 //     core reads (the tensor core has no product of a 16-bit and an 8-bit
 //     operand, and 8-bit queries or weights would lose what the state keeps),
 //     and computes each tile's scale factors and pads.
@@ -42,7 +42,7 @@ struct TcCfg {
   static constexpr int OFF_V = OFF_K + NS * TILE_BYTES;
   static constexpr int OFF_RAW = OFF_V + NS * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_RAW + NR * RAW_BYTES;
-  static constexpr int N_BARS = 2 + 4 * NS + 2 * NR + 2 + 2 + 2;
+  static constexpr int N_BARS = 2 + 4 * NS + NR + 2 + 2 + 2;
   static constexpr int OFF_FACT = OFF_BAR + ((N_BARS * 8 + 8 + 15) / 16) * 16;
   static constexpr int OFF_PAD = OFF_FACT + ((NF * 8 * 12 + 15) / 16) * 16;
   static constexpr int OFF_LIVE = OFF_PAD + NF * 128 * 4;
@@ -52,13 +52,12 @@ struct TcCfg {
   static_assert(256 + 2 * D <= 512, "TMEM columns");
 };
 
-constexpr int kTcThreads = 512;
-// 256 * 184 + 128 * 72 + 128 * 72 = 512 * 128
-constexpr uint32_t kTcSoftmaxRegs = 184, kTcControlRegs = 72, kTcWidenRegs = 72;
-static_assert(256 * kTcSoftmaxRegs + 128 * kTcControlRegs + 128 * kTcWidenRegs <= 512 * 128, "register split");
+constexpr int kTcThreads = 384;
+constexpr int kTcWidenThreads = 96;
+// 256 * 208 + 128 * 88 = 384 * 168
+constexpr uint32_t kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
+static_assert(256 * kTcSoftmaxRegs + 128 * kTcOtherRegs <= 384 * 168, "register split");
 constexpr uint64_t kTcDrainNs = 1000000000ull;
-// Pairs of columns (bit e of 16) whose exponentials go to the FMA pipe.
-constexpr uint32_t kTcFmaPairs = 0x8888u;
 
 __device__ __forceinline__ uint32_t tc_swizzle(uint32_t off, uint32_t layout) {
   return layout == 2u ? (off ^ (((off >> 7) & 7u) << 4)) : (off ^ (((off >> 7) & 3u) << 4));
@@ -77,21 +76,47 @@ __device__ __forceinline__ float lds32(uint32_t at) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
   return v;
 }
+__device__ __forceinline__ float2 lds64(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  return v;
+}
 __device__ __forceinline__ void sts32(uint32_t at, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0u;
+}
+
+// One arrival for the whole warp: 32 of them on one barrier serialise (at 256
+// for each query tile and 512 for the widening they were most of the time
+// between the last weight and the next product).
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// Barrier of `threads` threads that also tells all of them whether any has v.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(uint32_t(v))
+      : "memory");
+  return r != 0u;
 }
 
 // Instruction descriptor of kind::f16 with f16 A and B, fp32 accumulate.
 constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_major) {
   return (1u << 4) | (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
-}
-
-// Waits for this warp's TMEM loads and names the registers of one of them, so
-// that no use of it moves before the wait.
-__device__ __forceinline__ void tmem_landed(float (&x)[32]) {
-  tmem_wait_ld();
-#pragma unroll
-  for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(x[e]));
 }
 
 template <int D, bool PAD, bool E4M3>
@@ -106,13 +131,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   auto BAR = [&](int i) { return sb + uint32_t(C::OFF_BAR) + 8u * uint32_t(i); };
   constexpr int Q_FULL = 0, K_FULL = 2, K_EMPTY = K_FULL + C::NS, V_FULL = K_EMPTY + C::NS, V_EMPTY = V_FULL + C::NS,
-                RAW_FULL = V_EMPTY + C::NS, RAW_EMPTY = RAW_FULL + C::NR, S_FULL = RAW_EMPTY + C::NR,
+                RAW_FULL = V_EMPTY + C::NS, S_FULL = RAW_FULL + C::NR,
                 P_FULL = S_FULL + 2, O_FULL = P_FULL + 2, DRAIN = O_FULL + 1;
   static_assert(DRAIN + 1 == C::N_BARS, "barriers");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // uniform, so that what depends on the role alone stays in uniform registers
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   // CTAs below n_full take whole units; the others part (i % n_split) of unit
   // n_full + i / n_split
   const bool whole = int(blockIdx.x) < p.n_full;
@@ -169,30 +195,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
-      mbar_init(BAR(Q_FULL + t), 128);
+      mbar_init(BAR(Q_FULL + t), 4);
       mbar_init(BAR(S_FULL + t), 1);
-      mbar_init(BAR(P_FULL + t), 128);
+      mbar_init(BAR(P_FULL + t), 4);
     }
     for (int s = 0; s < C::NS; ++s) {
-      mbar_init(BAR(K_FULL + s), 128);
+      mbar_init(BAR(K_FULL + s), kTcWidenThreads / 32);
       mbar_init(BAR(K_EMPTY + s), 1);
-      mbar_init(BAR(V_FULL + s), 128);
+      mbar_init(BAR(V_FULL + s), kTcWidenThreads / 32);
       mbar_init(BAR(V_EMPTY + s), 1);
     }
     for (int s = 0; s < C::NR; ++s) {
       mbar_init(BAR(RAW_FULL + s), 1);
-      mbar_init(BAR(RAW_EMPTY + s), 128);
     }
     mbar_init(BAR(O_FULL), 1);
     mbar_init(BAR(DRAIN), 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
-  if (warp == 8) {
+  if (warp == 11) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (warp == 9 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
@@ -205,9 +230,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp < 8) {
     // ================================================== softmax warpgroups
     setmaxnreg_inc<kTcSoftmaxRegs>();
-    const int t = warp >> 2;
-    const int tid = threadIdx.x & 127;
-    const int my_row = row0 + t * 128 + tid;
+    const int t = warp >> 2;  // query tile
+    const int rr = threadIdx.x;  // row of the unit
+    const int my_row = row0 + rr;
     if (t == 0 || two) {
       int my_q = -1;
       if (my_row < p.n_rows) {
@@ -221,35 +246,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // swizzled K-major layout
       float undo;
       {
-        uint32_t w[D / 2];
-#pragma unroll
-        for (int c = 0; c < D / 2; ++c) w[c] = 0u;
-        if (my_q >= 0) {
-          const uint4* src =
-              reinterpret_cast<const uint4*>(p.q + b * p.q_sb + h * p.q_sh + int64_t(my_q) * p.q_sr);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = __ldg(src + c);
-            w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
-          }
-        }
+        uint4 v[D / 8];
         uint32_t m = 0u;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.q_sb + h * p.q_sh +
+                                                          int64_t(my_q < 0 ? 0 : my_q) * p.q_sr);
 #pragma unroll
-        for (int c = 0; c < D / 2; ++c) m = max(m, max((w[c] << 16) & 0x7FFF0000u, w[c] & 0x7FFF0000u));
+        for (int c = 0; c < D / 8; ++c) v[c] = my_q >= 0 ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m = max(m, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
+        }
         const float f = query_factor(m, p.scale_log2, undo);
         const uint32_t qs = sb + uint32_t(t * C::TILE_BYTES);
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
           uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            o[e] = pack_f16x2(__uint_as_float(w[4 * c + e] << 16) * f, __uint_as_float(w[4 * c + e] & 0xFFFF0000u) * f);
+            o[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
           const uint32_t off = uint32_t((c * 8 / C::CH) * C::CHUNK_BYTES) +
-                               tc_swizzle(uint32_t(tid * C::ROWB + (c * 8 % C::CH) * 2), C::LAYOUT);
+                               tc_swizzle(uint32_t((rr & 127) * C::ROWB + (c * 8 % C::CH) * 2), C::LAYOUT);
           sts128(qs + off, o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(BAR(Q_FULL + t));
+        warp_arrive(BAR(Q_FULL + t), lane);
       }
 
       const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
@@ -265,75 +288,64 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           break;
         }
         tc_fence_after();
+        float x[128];
+        {
+          uint32_t r[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + uint32_t(c * 32), r[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[c][e]);
+        }
         // factors of the tile's eight groups of 16 keys: ks, log2 vs, 1 / vs
         const uint32_t fact = sb + uint32_t(C::OFF_FACT + slot * 96);
         const uint32_t pads = sb + uint32_t(C::OFF_PAD + slot * 512);
         const int lim = p.Nk - j * C::BN;
         const bool ragged = !PAD && lim < C::BN;
-        // columns 32 c .. 32 c + 31: with pads, or past the last key, the raw
-        // scores become exponents undo ks x + pad here
-        auto shape = [&](int c, float (&x)[32]) {
-          if (PAD || ragged) {
+        float kf[8], lv[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float kf = undo * lds32(fact + uint32_t(((32 * c + e) / 16) * 4));
-              if constexpr (PAD) {
-                const uint4 pd = lds128(pads + uint32_t((32 * c + e) * 4));
-                x[e] = fmaf(x[e], kf, __uint_as_float(pd.x));
-                x[e + 1] = fmaf(x[e + 1], kf, __uint_as_float(pd.y));
-                x[e + 2] = fmaf(x[e + 2], kf, __uint_as_float(pd.z));
-                x[e + 3] = fmaf(x[e + 3], kf, __uint_as_float(pd.w));
-              } else {
+        for (int g = 0; g < 8; g += 4) {
+          const uint4 k4 = lds128(fact + uint32_t(g * 4)), l4 = lds128(fact + uint32_t(32 + g * 4));
+          kf[g] = undo * __uint_as_float(k4.x), kf[g + 1] = undo * __uint_as_float(k4.y);
+          kf[g + 2] = undo * __uint_as_float(k4.z), kf[g + 3] = undo * __uint_as_float(k4.w);
+          lv[g] = __uint_as_float(l4.x), lv[g + 1] = __uint_as_float(l4.y);
+          lv[g + 2] = __uint_as_float(l4.z), lv[g + 3] = __uint_as_float(l4.w);
+        }
+        tmem_wait_ld();
+        if (PAD || ragged) {  // exponents undo ks x + pad; kf has done its part
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[e + k] = 32 * c + e + k < lim ? x[e + k] * kf : -INFINITY;
-              }
+          for (int c = 0; c < 128; c += 4) {
+            if constexpr (PAD) {
+              const uint4 pd = lds128(pads + uint32_t(c * 4));
+              x[c] = fmaf(x[c], kf[c / 16], __uint_as_float(pd.x));
+              x[c + 1] = fmaf(x[c + 1], kf[c / 16], __uint_as_float(pd.y));
+              x[c + 2] = fmaf(x[c + 2], kf[c / 16], __uint_as_float(pd.z));
+              x[c + 3] = fmaf(x[c + 3], kf[c / 16], __uint_as_float(pd.w));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[c + e] = c + e < lim ? x[c + e] * kf[c / 16] : -INFINITY;
             }
           }
-        };
+#pragma unroll
+          for (int g = 0; g < 8; ++g) kf[g] = 1.f;
+        }
+        // The row's reference m follows the maximum lazily, by more than 2^8
+        // at a time.  (Taking the weights first and again where their sum says
+        // that m was too low saves the maximum, but keeps all 128 scores alive
+        // to the end: slower, for want of registers.)
         float mt = -INFINITY;
-        auto take_max = [&](int c, const float (&x)[32]) {
 #pragma unroll
-          for (int gg = 0; gg < 2; ++gg) {
-            const float* y = x + 16 * gg;
-            const int g = 2 * c + gg;
-            float m0 = max3(y[0], y[1], y[2]), m1 = max3(y[3], y[4], y[5]);
-            m0 = max3(m0, y[6], y[7]), m1 = max3(m1, y[8], y[9]);
-            m0 = max3(m0, y[10], y[11]), m1 = max3(m1, y[12], y[13]);
-            m0 = max3(m0, y[14], y[15]);
-            m0 = fmaxf(m0, m1);
-            const float lv = lds32(fact + uint32_t(32 + g * 4));
-            const float kf = PAD || ragged ? 1.f : undo * lds32(fact + uint32_t(g * 4));
-            mt = fmaxf(mt, fmaf(m0, kf, lv));
-          }
-        };
-        // The maximum needs all 128 columns before the first weight; half of
-        // them stay in registers, the others are read from TMEM again.
-        float x0[32], x1[32], x2[32];
-        auto load = [&](int c, float (&x)[32]) {
-          uint32_t r[32];
-          tmem_ld32(tS + uint32_t(c * 32), r);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
-        };
-        load(2, x0);
-        load(3, x1);
-        tmem_landed(x0);
-        tmem_landed(x1);
-        shape(2, x0);
-        take_max(2, x0);
-        shape(3, x1);
-        take_max(3, x1);
-        load(0, x0);
-        load(1, x1);
-        tmem_landed(x0);
-        tmem_landed(x1);
-        load(2, x2);
-        shape(0, x0);
-        take_max(0, x0);
-        shape(1, x1);
-        take_max(1, x1);
-        bool need_o = false;
+        for (int g = 0; g < 8; ++g) {
+          const float* y = x + 16 * g;
+          float m0 = max3(y[0], y[1], y[2]), m1 = max3(y[3], y[4], y[5]);
+          m0 = max3(m0, y[6], y[7]), m1 = max3(m1, y[8], y[9]);
+          m0 = max3(m0, y[10], y[11]), m1 = max3(m1, y[12], y[13]);
+          m0 = max3(m0, y[14], y[15]);
+          mt = fmaxf(mt, fmaf(fmaxf(m0, m1), kf[g], lv[g]));
+        }
         float alpha = 1.f;
+        bool need_o = false;
         if (mt > m_run + 8.f) {
           alpha = ex2_approx(m_run - mt);  // 0 from m = -inf
           l_run *= alpha;
@@ -341,42 +353,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           need_o = it > 0;
         }
         if (__any_sync(0xffffffffu, need_o)) {
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
+#pragma unroll 1
+          for (int e0 = 0; e0 < D; e0 += 16) {
             uint32_t r[16];
-            tmem_ld16(tO + uint32_t(c * 16), r);
+            tmem_ld16(tO + uint32_t(e0), r);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-            tmem_st16(tO + uint32_t(c * 16), r);
+            tmem_st16(tO + uint32_t(e0), r);
           }
         }
         const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
         const uint64_t negm2 = f2_pack(neg_m, neg_m);
-        auto emit = [&](int c, const float (&x)[32]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 inv = lds64(fact + uint32_t(64 + c * 8));
           uint32_t pk[16];
 #pragma unroll
           for (int gg = 0; gg < 2; ++gg) {
             const int g = 2 * c + gg;
-            const float lv = lds32(fact + uint32_t(32 + g * 4)), inv = lds32(fact + uint32_t(64 + g * 4));
-            const float kf = PAD || ragged ? 1.f : undo * lds32(fact + uint32_t(g * 4));
-            const float off = lv + neg_m;
-            const uint64_t kf2 = f2_pack(kf, kf), off2 = f2_pack(off, off), lv2 = f2_pack(lv, lv);
+            const float off = lv[g] + neg_m;
+            const uint64_t kf2 = f2_pack(kf[g], kf[g]), off2 = f2_pack(off, off), lv2 = f2_pack(lv[g], lv[g]);
             uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const uint64_t xx = f2_pack(x[16 * gg + 2 * e], x[16 * gg + 2 * e + 1]);
-              // with pads the difference to the maximum comes first: a pad of
-              // the type's lowest value absorbs everything added to it
+              const uint64_t xx = f2_pack(x[16 * g + 2 * e], x[16 * g + 2 * e + 1]);
+              // with pads the difference to the reference comes first: a pad
+              // of the type's lowest value absorbs everything added to it
               const uint64_t a2 = PAD ? f2_add(f2_add(xx, negm2), lv2) : f2_fma(xx, kf2, off2);
-              float a0, a1, p0, p1;
+              float a0, a1;
               f2_unpack(a2, a0, a1);
-              if (!PAD && ((kTcFmaPairs >> (8 * gg + e)) & 1u)) {
-                exp2_pair_fma(a0, a1, p0, p1);
-              } else {
-                p0 = ex2_approx(a0);
-                p1 = ex2_approx(a1);
-              }
+              const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
               if (e & 1)
                 s1 = f2_add(s1, f2_pack(p0, p1));
               else
@@ -385,23 +392,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             float u0, u1;
             f2_unpack(f2_add(s0, s1), u0, u1);
-            l_run = fmaf(u0 + u1, inv, l_run);
+            l_run = fmaf(u0 + u1, gg ? inv.y : inv.x, l_run);
           }
           tmem_st16(tS + uint32_t(c * 16), pk);
-        };
-        // weights of columns 32 c.. land in columns 16 c.. : behind the reads
-        emit(0, x0);
-        load(3, x0);
-        emit(1, x1);
-        tmem_landed(x2);
-        tmem_landed(x0);
-        shape(2, x2);
-        emit(2, x2);
-        shape(3, x0);
-        emit(3, x0);
+        }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(BAR(P_FULL + t));
+        warp_arrive(BAR(P_FULL + t), lane);
         j = next_live(j + 1);
         slot = slot + 1 == C::NF ? 0 : slot + 1;
       }
@@ -409,9 +406,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (ok && wait_warp(BAR(O_FULL), 0u, ctl)) {
         tc_fence_after();
         const bool live = my_q >= 0;
-        const bool empty = n_live == 0;  // O was never written
-        if (live && whole && l_run == 0.f) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        const bool empty = l_run == 0.f;  // O may never have been written
+        if (live && whole && empty) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
+        const float inv = empty ? 0.f : 1.f / l_run;
         float* po = nullptr;
         __nv_bfloat16* orow = nullptr;
         if (whole) {
@@ -419,25 +416,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           orow = p.out + b * p.o_sb + h * p.o_sh + at * p.o_sr;
         } else {
           const PartView pv = part_view(p, rest, D);
-          const int rr = t * 128 + tid;
           po = pv.o + int64_t(rr) * D;
           if (live) {
             pv.ml[rr * 2] = m_run;
             pv.ml[rr * 2 + 1] = l_run;
           }
         }
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
           uint32_t r[32];
-          tmem_ld32(tO + uint32_t(c * 32), r);
+          tmem_ld32(tO + uint32_t(c), r);
           tmem_wait_ld();
           if (!live) continue;
-          if (l_run == 0.f || empty) {
+          if (empty) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = 0u;
           }
           if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+            uint4* dst = reinterpret_cast<uint4*>(orow + c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t o[4];
@@ -447,198 +443,252 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               dst[e] = make_uint4(o[0], o[1], o[2], o[3]);
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(po + c * 32);
+            uint4* dst = reinterpret_cast<uint4*>(po + c);
 #pragma unroll
             for (int e = 0; e < 8; ++e) dst[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
           }
         }
       }
     }
-  } else if (warp < 12) {
-    setmaxnreg_dec<kTcControlRegs>();
-    if (warp == 8) {
-      // ================================================ TMA producer (codes)
-      if (lane == 0) {
-        int issued = 0;
-        const int n_live = live_count();
-        for (int it = 0, kt = next_live(k_lo); it < n_live; ++it, kt = next_live(kt + 1)) {
-          bool ok = true;
-          for (int kv = 0; kv < 2; ++kv) {
-            const int s = issued % C::NR;
-            if (!(ok = wait_bounded(BAR(RAW_EMPTY + s), uint32_t(((issued / C::NR) & 1) ^ 1), ctl))) break;
-            mbar_arrive_expect_tx(BAR(RAW_FULL + s), C::RAW_BYTES);
-            tma_load_4d(sb + uint32_t(C::OFF_RAW + s * C::RAW_BYTES), kv ? &tmV : &tmK, BAR(RAW_FULL + s), 0,
-                        kt * C::BN, h, b);
-            ++issued;
-          }
-          if (!ok) break;
-        }
-        // every copy has landed before the CTA leaves
-        for (int i = issued > C::NR ? issued - C::NR : 0; i < issued; ++i)
-          wait_drain(BAR(RAW_FULL + i % C::NR), uint32_t((i / C::NR) & 1), kTcDrainNs);
-      }
-    } else if (warp == 9) {
+  } else {
+    setmaxnreg_dec<kTcOtherRegs>();
+    if (warp == 11) {
       // ================================================ MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t idesc_qk = idesc_f16_f32(128, 128, 0), idesc_pv = idesc_f16_f32(128, D, 1);
-        constexpr uint32_t SBO = 8u * C::ROWB;
-        const uint64_t qd0 = smem_desc(sb, 16u, SBO, C::LAYOUT);
-        const uint64_t kd0 = smem_desc(sb + C::OFF_K, 16u, SBO, C::LAYOUT);
-        const uint64_t vd0 = smem_desc(sb + C::OFF_V, uint32_t(C::CHUNK_BYTES), SBO, C::LAYOUT);
-        auto adv = [](uint64_t d, uint32_t bytes) {
-          return (d & 0xFFFFFFFF00000000ull) | uint64_t(uint32_t(d) + (bytes >> 4));
-        };
-        auto issue_qk = [&](int t, int s) {
-          const uint64_t qd = adv(qd0, uint32_t(t * C::TILE_BYTES)), kd = adv(kd0, uint32_t(s * C::TILE_BYTES));
+      // The whole warp walks the loop and one elected lane issues, with the
+      // descriptors in uniform registers: with a single lane in the loop each
+      // of the 28 products of a tile took some 90 cycles to issue, which was
+      // two thirds of the tile's time.
+      constexpr uint32_t idesc_qk = idesc_f16_f32(128, 128, 0), idesc_pv = idesc_f16_f32(128, D, 1);
+      constexpr uint32_t SBO = 8u * C::ROWB;
+      const uint64_t qd0 = smem_desc(sb, 16u, SBO, C::LAYOUT);
+      const uint64_t kd0 = smem_desc(sb + C::OFF_K, 16u, SBO, C::LAYOUT);
+      const uint64_t vd0 = smem_desc(sb + C::OFF_V, uint32_t(C::CHUNK_BYTES), SBO, C::LAYOUT);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      // the address field of a descriptor advances in units of 16 bytes and
+      // stays below 2^14, so a 64-bit add does not carry out of it
+      auto issue_qk = [&](int t, int s) {
+        const uint64_t qd = qd0 + uint64_t(uint32_t(t * C::TILE_BYTES) >> 4), kd = kd0 + uint64_t(uint32_t(s * C::TILE_BYTES) >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = uint32_t(((kk * 16) / C::CH) * C::CHUNK_BYTES + ((kk * 16) % C::CH) * 2);
-            mma_ss(tmem + uint32_t(t * 128), adv(qd, off), adv(kd, off), idesc_qk, kk > 0 ? 1u : 0u);
+            const uint32_t off = uint32_t(((kk * 16) / C::CH) * C::CHUNK_BYTES + ((kk * 16) % C::CH) * 2) >> 4;
+            mma_ss(tm + uint32_t(t * 128), qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
           }
           tc_commit(BAR(S_FULL + t));
-        };
-        auto issue_pv = [&](int t, int s, bool acc) {
-          const uint64_t vd = adv(vd0, uint32_t(s * C::TILE_BYTES));
+        }
+      };
+      auto issue_pv = [&](int t, int s, bool acc) {
+        const uint64_t vd = vd0 + uint64_t(uint32_t(s * C::TILE_BYTES) >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < C::BN / 16; ++kk)
-            mma_ts(tmem + 256u + uint32_t(t * D), tmem + uint32_t(t * 128 + kk * 8), adv(vd, uint32_t(kk * 16 * C::ROWB)),
-                   idesc_pv, (acc || kk > 0) ? 1u : 0u);
-        };
-        const int n_live = live_count();
-        bool ok = wait_bounded(BAR(Q_FULL), 0u, ctl) && (!two || wait_bounded(BAR(Q_FULL + 1), 0u, ctl)) &&
-                  (n_live == 0 || wait_bounded(BAR(K_FULL), 0u, ctl));
-        if (ok && n_live > 0) {
-          tc_fence_after();
-          issue_qk(0, 0);
-          if (two) issue_qk(1, 0);
-          tc_commit(BAR(K_EMPTY));
+            mma_ts(tm + 256u + uint32_t(t * D), tm + uint32_t(t * 128 + kk * 8),
+                   vd + (uint32_t(kk * 16 * C::ROWB) >> 4), idesc_pv, (acc || kk > 0) ? 1u : 0u);
         }
-        for (int j = 0; ok && j < n_live; ++j) {
-          const int s = j % C::NS, s1 = (j + 1) % C::NS;
-          const bool more = j + 1 < n_live;
-          if (!(ok = wait_bounded(BAR(V_FULL + s), uint32_t((j / C::NS) & 1), ctl))) break;
-          if (!(ok = wait_bounded(BAR(P_FULL), uint32_t(j & 1), ctl))) break;
-          tc_fence_after();
-          issue_pv(0, s, j > 0);
-          if (more) {
-            if (!(ok = wait_bounded(BAR(K_FULL + s1), uint32_t(((j + 1) / C::NS) & 1), ctl))) break;
-            tc_fence_after();
-            issue_qk(0, s1);
-          }
-          if (two) {
-            if (!(ok = wait_bounded(BAR(P_FULL + 1), uint32_t(j & 1), ctl))) break;
-            tc_fence_after();
-            issue_pv(1, s, j > 0);
-          }
-          tc_commit(BAR(V_EMPTY + s));
-          if (more) {
-            if (two) issue_qk(1, s1);
-            tc_commit(BAR(K_EMPTY + s1));
-          }
-        }
-        if (ok) tc_commit(BAR(O_FULL));
-        // every MMA has completed before TMEM is freed, whoever aborted
-        tc_commit(BAR(DRAIN));
-        wait_drain(BAR(DRAIN), 0u, kTcDrainNs);
+      };
+      auto commit = [&](int bar) {
+        if (elect_one()) tc_commit(BAR(bar));
+      };
+      const int n_live = live_count();
+      bool ok = wait_warp(BAR(Q_FULL), 0u, ctl) && (!two || wait_warp(BAR(Q_FULL + 1), 0u, ctl)) &&
+                (n_live == 0 || wait_warp(BAR(K_FULL), 0u, ctl));
+      if (ok && n_live > 0) {
+        tc_fence_after();
+        issue_qk(0, 0);
+        if (two) issue_qk(1, 0);
+        commit(K_EMPTY);
       }
-    }
-  } else {
+      for (int j = 0; ok && j < n_live; ++j) {
+        const int s = j % C::NS, s1 = (j + 1) % C::NS;
+        const bool more = j + 1 < n_live;
+        if (!(ok = wait_warp(BAR(V_FULL + s), uint32_t((j / C::NS) & 1), ctl))) break;
+        if (!(ok = wait_warp(BAR(P_FULL), uint32_t(j & 1), ctl))) break;
+        tc_fence_after();
+        issue_pv(0, s, j > 0);
+        if (more) {
+          if (!(ok = wait_warp(BAR(K_FULL + s1), uint32_t(((j + 1) / C::NS) & 1), ctl))) break;
+          tc_fence_after();
+          issue_qk(0, s1);
+        }
+        if (two) {
+          if (!(ok = wait_warp(BAR(P_FULL + 1), uint32_t(j & 1), ctl))) break;
+          tc_fence_after();
+          issue_pv(1, s, j > 0);
+        }
+        commit(V_EMPTY + s);
+        if (more) {
+          if (two) issue_qk(1, s1);
+          commit(K_EMPTY + s1);
+        }
+      }
+      if (ok) commit(O_FULL);
+      // every MMA has completed before TMEM is freed, whoever aborted
+      commit(DRAIN);
+      wait_drain(BAR(DRAIN), 0u, kTcDrainNs);
+      __syncwarp();
+    } else {
     // ================================================ widening of the codes
-    setmaxnreg_dec<kTcWidenRegs>();
-    const int tid = threadIdx.x - 384;
+    const int tid = threadIdx.x - 256;
     const float* padb = PAD ? p.pad + b * p.pad_sb : nullptr;
     const float* ksb = p.ks + b * p.ks_sb + h * p.ks_sh;
     const float* vsb = p.vs + b * p.vs_sb + h * p.vs_sh;
     constexpr int UPR = D / 16;  // 16-code units per row
     float lv_lo = INFINITY, lv_hi = -INFINITY;
-    // raw tile -> f16 tile.  A unit becomes two 16-byte pieces; lanes of the
-    // row's second chunk write theirs in the other order, which keeps eight
-    // lanes on different banks.
+    // raw tile -> f16 tile, in units of 16 codes, each two 16-byte pieces of
+    // the f16 row, by 96 threads at offsets fixed for the kernel.
+    //   d = 96: thread r takes row r (stores of eight lanes fall on different
+    //     banks, loads two by two on the same); the last 32 rows go two units
+    //     to a thread.
+    //   d = 64, 128: units tid, tid + 96, ..: rows 24 or 12 apart, so the
+    //     swizzle is the first's or, every other time at d = 128, has its
+    //     third bit flipped.  Lanes of a row's second chunk write their pieces
+    //     in the other order, which keeps eight lanes on different banks.
+    auto place = [&](uint4 v, uint32_t a0, uint32_t a1) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t o[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x = bias_codes<E4M3>(w[e]);
+        o[2 * e] = widen_lo<E4M3>(x);
+        o[2 * e + 1] = widen_hi<E4M3>(x);
+      }
+      sts128(a0, o[0], o[1], o[2], o[3]);
+      sts128(a1, o[4], o[5], o[6], o[7]);
+    };
+    // masked keys: zeros, whatever the codes (NaN) are
+    auto clear_dead = [&](uint4& v, int key) {
+      if constexpr (PAD) {
+        if (key < p.Nk && __ldg(padb + key) == -INFINITY) v = make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    constexpr int RPP = kTcWidenThreads / UPR;  // d = 64, 128: rows a pass
+    const int u_row = tid / UPR, u_col = tid % UPR;
+    const bool swap = D != 96 && ((u_col * 16 / C::CH) & 1);
+    const uint32_t in_row = uint32_t(u_row * C::ROWB + (u_col * 16 % C::CH) * 2);
+    const uint32_t chunk0 = uint32_t((u_col * 16 / C::CH) * C::CHUNK_BYTES);
+    const uint32_t p0 = chunk0 + tc_swizzle(in_row + (swap ? 16u : 0u), C::LAYOUT);
+    const uint32_t p1 = chunk0 + tc_swizzle(in_row + (swap ? 0u : 16u), C::LAYOUT);
+    // the loads of four units go out before the first is widened
     auto widen = [&](uint32_t raw, uint32_t to, int key0) {
+      if constexpr (D == 96) {
 #pragma unroll
-      for (int i = 0; i < UPR; ++i) {
-        const int u = tid + i * 128;
-        const int r = u / UPR, c = u - r * UPR;
-        uint4 v = lds128(raw + uint32_t(u * 16));
-        if constexpr (PAD) {  // masked keys: zeros, whatever the codes (NaN) are
-          const int key = key0 + r;
-          if (key < p.Nk && __ldg(padb + key) == -INFINITY) v = make_uint4(0u, 0u, 0u, 0u);
-        }
-        uint32_t w[4] = {v.x, v.y, v.z, v.w}, o[8];
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+          uint4 v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t x = bias_codes<E4M3>(w[e]);
-          o[2 * e] = widen_lo<E4M3>(x);
-          o[2 * e + 1] = widen_hi<E4M3>(x);
+          for (int i = 0; i < 4; ++i) {
+            const int r = i0 + i < 6 ? tid : 96 + lane, c = i0 + i < 6 ? i0 + i : (tid >> 5) * 2 + i0 + i - 6;
+            v[i] = lds128(raw + uint32_t(r * D + c * 16));
+            clear_dead(v[i], key0 + r);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = i0 + i < 6 ? tid : 96 + lane, c = i0 + i < 6 ? i0 + i : (tid >> 5) * 2 + i0 + i - 6;
+            const uint32_t in = uint32_t(r * C::ROWB + (c & 1) * 32), base = to + uint32_t((c / 2) * C::CHUNK_BYTES);
+            place(v[i], base + tc_swizzle(in, C::LAYOUT), base + tc_swizzle(in + 16u, C::LAYOUT));
+          }
         }
-        const int chunk = c * 16 / C::CH;
-        const uint32_t row = uint32_t(r * C::ROWB + (c * 16 % C::CH) * 2);
-        const uint32_t base = to + uint32_t(chunk * C::CHUNK_BYTES);
-        const uint32_t a0 = base + tc_swizzle(row, C::LAYOUT), a1 = base + tc_swizzle(row + 16u, C::LAYOUT);
-        if (chunk & 1) {
-          sts128(a1, o[4], o[5], o[6], o[7]);
-          sts128(a0, o[0], o[1], o[2], o[3]);
-        } else {
-          sts128(a0, o[0], o[1], o[2], o[3]);
-          sts128(a1, o[4], o[5], o[6], o[7]);
+      } else {
+        constexpr int PASSES = (128 + RPP - 1) / RPP;
+#pragma unroll
+        for (int i0 = 0; i0 < PASSES; i0 += 4) {
+          uint4 v[4];
+#pragma unroll
+          for (int i = i0; i < i0 + 4 && i < PASSES; ++i) {
+            if (i + 1 < PASSES || u_row + i * RPP < 128) {
+              v[i - i0] = lds128(raw + uint32_t(tid * 16 + i * RPP * D));
+              clear_dead(v[i - i0], key0 + u_row + i * RPP);
+            }
+          }
+#pragma unroll
+          for (int i = i0; i < i0 + 4 && i < PASSES; ++i) {
+            if (i + 1 < PASSES || u_row + i * RPP < 128) {
+              const uint4 x = v[i - i0];
+              const uint32_t flip = (RPP * i) & 4 ? 64u : 0u, at = to + uint32_t(i * RPP * C::ROWB);
+              place(swap ? make_uint4(x.z, x.w, x.x, x.y) : x, at + (p0 ^ flip), at + (p1 ^ flip));
+            }
+          }
         }
       }
     };
+    // Raw tiles come by TMA into a ring, K and V of a key tile in turn: tile n
+    // of them goes to slot n % NR.  Thread 0 issues, tile n + NR once the
+    // group's barrier says that tile n has been read.
     const int n_live = live_count();
+    int issued = 0, kt_load = next_live(k_lo);
+    auto load_next = [&]() {  // thread 0
+      if (issued >= 2 * n_live) return;
+      const int s = issued % C::NR;
+      mbar_arrive_expect_tx(BAR(RAW_FULL + s), C::RAW_BYTES);
+      tma_load_4d(sb + uint32_t(C::OFF_RAW + s * C::RAW_BYTES), issued & 1 ? &tmV : &tmK, BAR(RAW_FULL + s), 0,
+                  kt_load * C::BN, h, b);
+      if (issued & 1) kt_load = next_live(kt_load + 1);
+      ++issued;
+    };
+    if (tid == 0)
+      for (int n = 0; n < C::NR; ++n) load_next();
+    bool ok = true;
     int slot = 0;
-    for (int it = 0, kt = next_live(k_lo); it < n_live; ++it, kt = next_live(kt + 1)) {
+    for (int it = 0, kt = next_live(k_lo); ok && it < n_live; ++it, kt = next_live(kt + 1)) {
       const int s = it % C::NS;
       const uint32_t ph = uint32_t((it / C::NS) & 1) ^ 1u;
       const int key0 = kt * C::BN;
-      int n = 2 * it;
-      if (!wait_warp(BAR(RAW_FULL + n % C::NR), uint32_t((n / C::NR) & 1), ctl)) break;
-      if (!wait_warp(BAR(K_EMPTY + s), ph, ctl)) break;
-      // Scale factors and pads of the tile, NS + 1 slots: when the K tile
-      // `it - NS` is free, its scores are done, which took the weights of
-      // tile `it - NS - 1` from both query tiles, so nobody reads a slot
-      // older than `it - NS`.
-      if (tid < 8) {
-        const int key = key0 + tid * 16;
-        float ks = 0.f, lv = 0.f;
-        if (key < p.Nk) {
-          ks = __ldg(ksb + (key >> p.block_log2));
-          const float vs = __ldg(vsb + (key >> p.block_log2));
-          lv = __log2f(vs);
-          bool used = true;  // a key of the group that is not masked
-          if (!(ks >= 0.f && ks < INFINITY && vs > 0.f && vs < INFINITY)) {
-            if constexpr (PAD) {
-              used = false;
-              for (int e = 0; e < 16 && key + e < p.Nk; ++e) used |= __ldg(padb + key + e) != -INFINITY;
+      for (int kv = 0; ok && kv < 2; ++kv) {
+        const int n = 2 * it + kv, raw = n % C::NR;
+        ok = wait_warp(BAR(RAW_FULL + raw), uint32_t((n / C::NR) & 1), ctl) &&
+             wait_warp(BAR((kv ? V_EMPTY : K_EMPTY) + s), ph, ctl);
+        if (ok && kv == 0) {
+          // Scale factors and pads of the tile, NS + 1 slots: when the K tile
+          // `it - NS` is free, its scores are done, which took the weights of
+          // tile `it - NS - 1` from both query tiles, so nobody reads a slot
+          // older than `it - NS`.
+          if (tid < 8) {
+            const int key = key0 + tid * 16;
+            float ks = 0.f, lv = 0.f;
+            if (key < p.Nk) {
+              ks = __ldg(ksb + (key >> p.block_log2));
+              const float vs = __ldg(vsb + (key >> p.block_log2));
+              lv = __log2f(vs);
+              if (!(ks >= 0.f && ks < INFINITY && vs > 0.f && vs < INFINITY)) {
+                bool used = true;  // a key of the group that is not masked
+                if constexpr (PAD) {
+                  used = false;
+                  for (int e = 0; e < 16 && key + e < p.Nk; ++e) used |= __ldg(padb + key + e) != -INFINITY;
+                }
+                if (used) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
+                else ks = 0.f, lv = 0.f;
+              } else {
+                lv_lo = fminf(lv_lo, lv);
+                lv_hi = fmaxf(lv_hi, lv);
+              }
             }
-            if (used) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
-            else ks = 0.f, lv = 0.f;
-          } else {
-            lv_lo = fminf(lv_lo, lv);
-            lv_hi = fmaxf(lv_hi, lv);
+            const uint32_t f = sb + uint32_t(C::OFF_FACT + slot * 96 + tid * 4);
+            sts32(f, ks);
+            sts32(f + 32u, lv);
+            sts32(f + 64u, ex2_approx(-lv));
+          }
+          if constexpr (PAD) {
+            for (int e = tid; e < C::BN; e += kTcWidenThreads)
+              sts32(sb + uint32_t(C::OFF_PAD + slot * 512 + e * 4),
+                    key0 + e < p.Nk ? pad_log2(__ldg(padb + key0 + e)) : -INFINITY);
           }
         }
-        const uint32_t f = sb + uint32_t(C::OFF_FACT + slot * 96 + tid * 4);
-        sts32(f, ks);
-        sts32(f + 32u, lv);
-        sts32(f + 64u, ex2_approx(-lv));
+        if (ok) {
+          widen(sb + uint32_t(C::OFF_RAW + raw * C::RAW_BYTES),
+                sb + uint32_t((kv ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES), key0);
+          fence_proxy_async_smem();
+          warp_arrive(BAR((kv ? V_FULL : K_FULL) + s), lane);
+        }
+        ok = !bar_any(1, kTcWidenThreads, !ok);  // read by all three warps, or given up by all
+        if (ok && tid == 0) load_next();
       }
-      if constexpr (PAD)
-        sts32(sb + uint32_t(C::OFF_PAD + slot * 512 + tid * 4),
-              key0 + tid < p.Nk ? pad_log2(__ldg(padb + key0 + tid)) : -INFINITY);
-      widen(sb + uint32_t(C::OFF_RAW + (n % C::NR) * C::RAW_BYTES), sb + uint32_t(C::OFF_K + s * C::TILE_BYTES), key0);
-      mbar_arrive(BAR(RAW_EMPTY + n % C::NR));
-      fence_proxy_async_smem();
-      mbar_arrive(BAR(K_FULL + s));
-      ++n;
-      if (!wait_warp(BAR(RAW_FULL + n % C::NR), uint32_t((n / C::NR) & 1), ctl)) break;
-      if (!wait_warp(BAR(V_EMPTY + s), ph, ctl)) break;
-      widen(sb + uint32_t(C::OFF_RAW + (n % C::NR) * C::RAW_BYTES), sb + uint32_t(C::OFF_V + s * C::TILE_BYTES), key0);
-      mbar_arrive(BAR(RAW_EMPTY + n % C::NR));
-      fence_proxy_async_smem();
-      mbar_arrive(BAR(V_FULL + s));
       slot = slot + 1 == C::NF ? 0 : slot + 1;
     }
-    if (warp == 12) {
+    // every copy has landed before the CTA leaves
+    if (tid == 0)
+      for (int i = issued > C::NR ? issued - C::NR : 0; i < issued; ++i)
+        wait_drain(BAR(RAW_FULL + i % C::NR), uint32_t((i / C::NR) & 1), kTcDrainNs);
+    __syncwarp();
+    if (warp == 8) {
 #pragma unroll
       for (int e = 1; e < 8; e <<= 1) {
         lv_lo = fminf(lv_lo, __shfl_xor_sync(0xffffffffu, lv_lo, e));
@@ -654,11 +704,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
+    }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 11) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
