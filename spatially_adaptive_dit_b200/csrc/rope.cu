@@ -75,7 +75,9 @@ safedit_status rope_setup(const safedit_rope* rope, const safedit_tensor* pos, i
 
 constexpr int kMaxRopeTensors = 4;
 constexpr int kRopeThreads = 256;
-constexpr int kRopeFlight = 4;  // heads whose loads are in flight in one thread
+// heads whose loads are in flight in one thread: 128 bytes of them
+template <typename T>
+constexpr int kRopeFlight = sizeof(T) == 4 ? 4 : 8;
 
 struct RopeParams {
   RopeTable tab;
@@ -113,11 +115,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
   float c[4], s[4];
   rope_angles(p.tab, p.pos, b, i, slot, p.sign, c, s);
   const int h_end = min(p.n_heads, int(blockIdx.y + 1) * p.heads_per_group);
-  for (int h0 = blockIdx.y * p.heads_per_group; h0 < h_end; h0 += kRopeFlight) {
-    uint32_t w[kRopeFlight][SlotWords<T>::N];
-    T* to[kRopeFlight];
+  constexpr int F = kRopeFlight<T>;
+  for (int h0 = blockIdx.y * p.heads_per_group; h0 < h_end; h0 += F) {
+    uint32_t w[F][SlotWords<T>::N];
+    T* to[F];
 #pragma unroll
-    for (int e = 0; e < kRopeFlight; ++e) {
+    for (int e = 0; e < F; ++e) {
       const int hh = h0 + e;
       if (hh >= h_end) break;
       int t = 0;
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
       slot_load<T, HALVES>(w[e], row, lo, hi);
     }
 #pragma unroll
-    for (int e = 0; e < kRopeFlight; ++e) {
+    for (int e = 0; e < F; ++e) {
       if (h0 + e >= h_end) break;
       float x[8];
       slot_widen<T>(w[e], x);
@@ -232,9 +235,10 @@ extern "C" safedit_status safedit_rope_rows(const safedit_tensor* src, const saf
   if (d_idx && dst_indexed && index_check_enabled() &&
       (st = launch_index_check(d_idx, int32_t(n), p.limit, p.status, s)) != SAFEDIT_OK)
     return st;
-  // as few head groups as still give every SM eight blocks
-  const int64_t want = (8 * 148 + blocks * B - 1) / (blocks * B);
-  int64_t groups = (heads + kRopeFlight - 1) / kRopeFlight;
+  // as few head groups as still give every SM two blocks: each group pays for
+  // the angles again
+  const int64_t want = (2 * 148 + blocks * B - 1) / (blocks * B);
+  int64_t groups = (heads + 3) / 4;
   if (groups > want) groups = want;
   p.heads_per_group = int((heads + groups - 1) / groups);
   groups = (heads + p.heads_per_group - 1) / p.heads_per_group;

@@ -32,8 +32,8 @@ struct StoreParams {
   int64_t c_sb[kMaxStoreTensors], c_sh[kMaxStoreTensors], c_sr[kMaxStoreTensors];
   int64_t f_sb[kMaxStoreTensors], f_sh[kMaxStoreTensors];
   int rotate[kMaxStoreTensors];
-  int head_end[kMaxStoreTensors];
-  int n_heads, heads_per_group, any_rotate, slots, e4m3;
+  int heads[kMaxStoreTensors], group_end[kMaxStoreTensors];  // head groups of tensors 0..t together
+  int heads_per_group, any_rotate, slots, e4m3;
   int n_rows, row0, state_rows;
   int64_t limit;
   const int* idx;
@@ -65,10 +65,19 @@ struct StoreCfg {
   static constexpr int RP = BLOCK <= 32 ? 16 : 32;
   static constexpr int R = BLOCK / RP;
   static constexpr int MAX_THREADS = RP * 16;
+  // 64 registers a thread up to two rows, 128 for four
+  static constexpr int MIN_CTAS = (R <= 2 ? 1024 : 512) / MAX_THREADS;
 };
 
+// max(m, |a|, |b|), NaN if one is.
+__device__ __forceinline__ float max_abs3(float m, float a, float b) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
+}
+
 template <typename T, int BLOCK, bool HALVES>
-__global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS)
+__global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>::MIN_CTAS)
     state8_store_kernel(const __grid_constant__ StoreParams p) {
   using C = StoreCfg<BLOCK>;
   constexpr int NW = SlotWords<T>::N;
@@ -78,85 +87,82 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS)
   const int lane = threadIdx.x & 31, warps = int(blockDim.x) >> 5;
   const int b = blockIdx.z;
   const int r0 = blockIdx.x * BLOCK;
+  // this CTA's tensor and heads
+  int t = 0;
+  while (int(blockIdx.y) >= p.group_end[t]) ++t;
+  const int group = int(blockIdx.y) - (t ? p.group_end[t - 1] : 0);
+  const int h_begin = group * p.heads_per_group, h_end = min(p.heads[t], h_begin + p.heads_per_group);
+  const bool rotate = p.rotate[t];
   int lo = slot * 8, hi = slot * 8 + 4;
   if (HALVES && p.any_rotate) lo = p.tab.lo[slot], hi = p.tab.hi[slot];
-  int64_t from[C::R];  // source row, -1: none (its codes are zero)
+  const T* from[C::R];  // source row of head h, null: none (its codes are zero)
   float c[C::R][4], s[C::R][4];
+  const T* base = static_cast<const T*>(p.src[t]) + b * p.s_sb[t] + h_begin * p.s_sh[t];
 #pragma unroll
   for (int k = 0; k < C::R; ++k) {
     const int r = r0 + rr + k * C::RP;
-    from[k] = -1;
+    from[k] = nullptr;
     int64_t i = r;
     if (r < p.n_rows) {
-      from[k] = r;
-      if (p.idx) {
-        i = __ldg(p.idx + r);
-        const bool in = i >= 0 && i < p.limit;
-        if (!in) set_status(p.status, SAFEDIT_ERR_INDEX);
-        from[k] = !in ? -1 : p.src_indexed ? i : r;
-      }
+      if (p.idx) i = __ldg(p.idx + r);
+      if (p.idx && (i < 0 || i >= p.limit)) set_status(p.status, SAFEDIT_ERR_INDEX);
+      else from[k] = base + (p.src_indexed ? i : int64_t(r)) * p.s_sr[t];
     }
-    if (p.any_rotate) {
-      if (from[k] >= 0) {
-        rope_angles(p.tab, p.pos, b, i, slot, 1.f, c[k], s[k]);
-      } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[k][j] = 1.f, s[k][j] = 0.f;
-      }
-    }
+    for (int j = 0; j < 4; ++j) c[k][j] = 1.f, s[k][j] = 0.f;
+    if (rotate && from[k]) rope_angles(p.tab, p.pos, b, i, slot, 1.f, c[k], s[k]);
   }
-  const int h_begin = blockIdx.y * p.heads_per_group;
-  const int h_end = min(p.n_heads, h_begin + p.heads_per_group);
   uint32_t w[C::R][NW];
-  auto tensor_of = [&](int hh, int& t, int& h) {
-    t = 0;
-    while (hh >= p.head_end[t]) ++t;
-    h = t ? hh - p.head_end[t - 1] : hh;
-  };
-  auto load = [&](int hh) {
-    int t, h;
-    tensor_of(hh, t, h);
-    const T* base = static_cast<const T*>(p.src[t]) + b * p.s_sb[t] + h * p.s_sh[t];
+  auto load = [&]() {
 #pragma unroll
     for (int k = 0; k < C::R; ++k) {
 #pragma unroll
       for (int e = 0; e < NW; ++e) w[k][e] = 0u;
-      if (from[k] >= 0) slot_load<T, HALVES>(w[k], base + from[k] * p.s_sr[t], lo, hi);
+      if (from[k]) {
+        slot_load<T, HALVES>(w[k], from[k], lo, hi);
+        from[k] += p.s_sh[t];
+      }
     }
   };
-  load(h_begin);
-  for (int hh = h_begin; hh < h_end; ++hh) {
-    int t, h;
-    tensor_of(hh, t, h);
+  const int first = p.row0 + r0 + rr;  // state row of the thread's first row
+  uint8_t* to = p.code[t] + b * p.c_sb[t] + h_begin * p.c_sh[t] + int64_t(first) * p.c_sr[t];
+  float* to_scale = p.scale[t] + b * p.f_sb[t] + h_begin * p.f_sh[t] + p.row0 / BLOCK + blockIdx.x;
+  load();
+  for (int h = h_begin; h < h_end; ++h) {
     float x[C::R][8];
 #pragma unroll
     for (int k = 0; k < C::R; ++k) slot_widen<T>(w[k], x[k]);
-    if (hh + 1 < h_end) load(hh + 1);
-    if (p.rotate[t]) {
+    if (h + 1 < h_end) load();
+    if (rotate) {
 #pragma unroll
       for (int k = 0; k < C::R; ++k) rope_turn<HALVES>(x[k], c[k], s[k]);
     }
     // largest magnitude of the block: the bits of |x| order as integers, and
     // infinities and NaN come out on top
-    auto block_max = [&](bool finite_only, int buf) {
-      uint32_t m = 0u;
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < C::R; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) m = max_abs3(m, x[k][e], x[k][e + 1]);
+    const int buf = (h - h_begin) & 1;
+    auto over_block = [&](uint32_t bits) {
+      bits = __reduce_max_sync(0xffffffffu, bits);
+      if (lane == 0) part[buf][threadIdx.x >> 5] = bits;
+      __syncthreads();
+      return __reduce_max_sync(0xffffffffu, lane < warps ? part[buf][lane] : 0u);
+    };
+    uint32_t top = over_block(__float_as_uint(m) & 0x7FFFFFFFu);
+    if (top >= 0x7F800000u) {  // infinities saturate, NaN becomes 0; reported
+      uint32_t f = 0u;
 #pragma unroll
       for (int k = 0; k < C::R; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const uint32_t a = __float_as_uint(x[k][e]) & 0x7FFFFFFFu;
-          m = max(m, finite_only && a >= 0x7F800000u ? 0u : a);
+          f = max(f, a >= 0x7F800000u ? 0u : a);
         }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) part[buf][threadIdx.x >> 5] = m;
       __syncthreads();
-      return __reduce_max_sync(0xffffffffu, lane < warps ? part[buf][lane] : 0u);
-    };
-    const int buf = (hh - h_begin) & 1;
-    uint32_t top = block_max(false, buf);
-    if (top >= 0x7F800000u) {  // infinities saturate, NaN becomes 0; reported
-      __syncthreads();
-      top = block_max(true, buf);
+      top = over_block(f);
       if (threadIdx.x == 0) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
       const float big = top ? __uint_as_float(top) : qmax;
 #pragma unroll
@@ -171,8 +177,7 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS)
         }
     }
     const float most = top ? fmaxf(__uint_as_float(top), kLeastMax) : qmax;
-    if (threadIdx.x == 0)
-      p.scale[t][b * p.f_sb[t] + h * p.f_sh[t] + p.row0 / BLOCK + blockIdx.x] = most / qmax;
+    if (threadIdx.x == 0) *to_scale = most / qmax;
     // x qmax / most with one rounding: both sides by the power of two that
     // brings `most` into [1, 2) (exact), then Markstein's correction of
     // x * RN(1 / most).  With 16-bit rows the product x qmax is exact, so a
@@ -182,17 +187,16 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS)
     const float m1 = __uint_as_float((__float_as_uint(most) & 0x007FFFFFu) | 0x3F800000u);
     const float up = __uint_as_float(uint32_t(127 + 6 - ex) << 23) * (qmax / 64.f);  // qmax 2^-ex, exact
     const float inv = 1.f / m1;
-    uint8_t* crow = p.code[t] + b * p.c_sb[t] + h * p.c_sh[t];
+    const uint64_t up2 = f2_pack(up, up), inv2 = f2_pack(inv, inv), neg2 = f2_pack(-m1, -m1);
 #pragma unroll
     for (int k = 0; k < C::R; ++k) {
-      const int dst = p.row0 + r0 + rr + k * C::RP;
-      if (dst >= p.state_rows) continue;
+      if (first + k * C::RP >= p.state_rows) continue;
       float y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float a = x[k][e] * up;
-        const float q = a * inv;
-        y[e] = fmaf(fmaf(-q, m1, a), inv, q);
+      for (int e = 0; e < 8; e += 2) {
+        const uint64_t a = f2_mul(f2_pack(x[k][e], x[k][e + 1]), up2);
+        const uint64_t q = f2_mul(a, inv2);
+        f2_unpack(f2_fma(f2_fma(q, neg2, a), inv2, q), y[e], y[e + 1]);
       }
       uint32_t o0, o1;
       if (p.e4m3) {
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS)
         o0 = pack_codes<false>(y[0], y[1], y[2], y[3]);
         o1 = pack_codes<false>(y[4], y[5], y[6], y[7]);
       }
-      uint8_t* row = crow + int64_t(dst) * p.c_sr[t];
+      uint8_t* row = to + int64_t(k * C::RP) * p.c_sr[t];
       if constexpr (HALVES) {
         *reinterpret_cast<uint32_t*>(row + lo) = o0;
         *reinterpret_cast<uint32_t*>(row + hi) = o1;
@@ -210,19 +214,24 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS)
         *reinterpret_cast<uint2*>(row + lo) = make_uint2(o0, o1);
       }
     }
+    to += p.c_sh[t];
+    to_scale += p.f_sh[t];
   }
 }
 
 template <typename T, int BLOCK, bool HALVES>
-static safedit_status launch_store(StoreParams& p, int64_t B, cudaStream_t s) {
+static safedit_status launch_store(StoreParams& p, int64_t B, int64_t n_heads, int n_tensors, cudaStream_t s) {
   const int threads = StoreCfg<BLOCK>::RP * p.slots;
   const int64_t blocks = (int64_t(p.n_rows) + BLOCK - 1) / BLOCK;
   // as few head groups as still give every SM 2048 threads twice over
   const int64_t ctas = 148 * 2 * (2048 / threads);
-  int64_t groups = (ctas + blocks * B - 1) / (blocks * B);
-  if (groups > p.n_heads) groups = p.n_heads;
-  p.heads_per_group = int((p.n_heads + groups - 1) / groups);
-  groups = (p.n_heads + p.heads_per_group - 1) / p.heads_per_group;
+  int64_t want = (ctas + blocks * B - 1) / (blocks * B);
+  p.heads_per_group = int((n_heads + want - 1) / want);
+  int64_t groups = 0;
+  for (int t = 0; t < n_tensors; ++t) {
+    groups += (p.heads[t] + p.heads_per_group - 1) / p.heads_per_group;
+    p.group_end[t] = int(groups);
+  }
   if (groups > 65535) return SAFEDIT_ERR_UNSUPPORTED;
   state8_store_kernel<T, BLOCK, HALVES>
       <<<dim3(unsigned(blocks), unsigned(groups), unsigned(B)), threads, 0, s>>>(p);
@@ -230,18 +239,20 @@ static safedit_status launch_store(StoreParams& p, int64_t B, cudaStream_t s) {
 }
 
 template <typename T, bool HALVES>
-static safedit_status store_by_block(StoreParams& p, int64_t B, int block, cudaStream_t s) {
+static safedit_status store_by_block(StoreParams& p, int64_t B, int64_t n_heads, int n_tensors, int block, cudaStream_t s) {
   switch (block) {
-    case 16: return launch_store<T, 16, HALVES>(p, B, s);
-    case 32: return launch_store<T, 32, HALVES>(p, B, s);
-    case 64: return launch_store<T, 64, HALVES>(p, B, s);
-    default: return launch_store<T, 128, HALVES>(p, B, s);
+    case 16: return launch_store<T, 16, HALVES>(p, B, n_heads, n_tensors, s);
+    case 32: return launch_store<T, 32, HALVES>(p, B, n_heads, n_tensors, s);
+    case 64: return launch_store<T, 64, HALVES>(p, B, n_heads, n_tensors, s);
+    default: return launch_store<T, 128, HALVES>(p, B, n_heads, n_tensors, s);
   }
 }
 
 template <typename T>
-static safedit_status store_by_form(StoreParams& p, int64_t B, int block, bool halves, cudaStream_t s) {
-  return halves ? store_by_block<T, true>(p, B, block, s) : store_by_block<T, false>(p, B, block, s);
+static safedit_status store_by_form(StoreParams& p, int64_t B, int64_t n_heads, int n_tensors, int block, bool halves,
+                                    cudaStream_t s) {
+  return halves ? store_by_block<T, true>(p, B, n_heads, n_tensors, block, s)
+                : store_by_block<T, false>(p, B, n_heads, n_tensors, block, s);
 }
 
 }  // namespace sd
@@ -284,7 +295,7 @@ extern "C" safedit_status safedit_state8_store(const safedit_tensor* src, const 
     p.s_sb[t] = x.strides[0], p.s_sh[t] = x.strides[1], p.s_sr[t] = x.strides[2];
     p.c_sb[t] = c.strides[0], p.c_sh[t] = c.strides[1], p.c_sr[t] = c.strides[2];
     p.f_sb[t] = f.strides[0], p.f_sh[t] = f.strides[1];
-    p.head_end[t] = int(heads);
+    p.heads[t] = int(x.dims[1]);
     p.rotate[t] = host_rotate ? host_rotate[t] : 0;
     if (p.rotate[t] != 0 && p.rotate[t] != 1) return SAFEDIT_ERR_INVALID_ARG;
     p.any_rotate |= p.rotate[t];
@@ -304,7 +315,6 @@ extern "C" safedit_status safedit_state8_store(const safedit_tensor* src, const 
     for (int t = 0; t < n_tensors; ++t)
       if (src[t].dims[2] < p.limit) p.limit = src[t].dims[2];
   if (n == 0 || B == 0 || heads == 0) return SAFEDIT_OK;
-  p.n_heads = int(heads);
   p.slots = int(d / 8);
   p.e4m3 = codes[0].dtype == SAFEDIT_E4M3;
   p.n_rows = int(n);
@@ -317,8 +327,8 @@ extern "C" safedit_status safedit_state8_store(const safedit_tensor* src, const 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool halves = p.any_rotate && rope->halves;
   switch (src[0].dtype) {
-    case SAFEDIT_BF16: return store_by_form<__nv_bfloat16>(p, B, block, halves, s);
-    case SAFEDIT_F16: return store_by_form<__half>(p, B, block, halves, s);
-    default: return store_by_form<float>(p, B, block, halves, s);
+    case SAFEDIT_BF16: return store_by_form<__nv_bfloat16>(p, B, heads, n_tensors, block, halves, s);
+    case SAFEDIT_F16: return store_by_form<__half>(p, B, heads, n_tensors, block, halves, s);
+    default: return store_by_form<float>(p, B, heads, n_tensors, block, halves, s);
   }
 }
