@@ -137,8 +137,14 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without building a torch.cuda.Stream (0.1 us against 4.8 us, a third of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
@@ -255,23 +261,26 @@ def safedit_gemm_bias_act(a, w, bias, act, idx_out, out, stream=None):
 _TENSOR = struct.Struct("Pii8q")
 _TENSOR3 = struct.Struct("Pii3q8x3q8x")
 assert _TENSOR.size == _TENSOR3.size == ctypes.sizeof(SafeditTensor)
+_pack4, _pack3 = _TENSOR.pack, _TENSOR3.pack
 
 
 def _packed(t, device):
     """`t` as the bytes of a safedit_tensor; it has to live on the current device (number `device`)."""
     if t.get_device() != device:
         raise SafeditError(ERR_INVALID_ARG, f"a tensor on {t.device}, with cuda:{device} the current device")
-    if t.dtype not in _DTYPE:
+    code = _DTYPE.get(t.dtype)
+    if code is None:
         raise SafeditError(ERR_DTYPE, f"a tensor of {t.dtype}")
-    n = t.dim()
+    shape = t.shape
+    n = len(shape)
     if n == 4:
-        return _TENSOR.pack(t.data_ptr(), _DTYPE[t.dtype], 4, *t.shape, *t.stride())
+        return _pack4(t.data_ptr(), code, 4, *shape, *t.stride())
     if n == 3:
-        return _TENSOR3.pack(t.data_ptr(), _DTYPE[t.dtype], 3, *t.shape, *t.stride())
+        return _pack3(t.data_ptr(), code, 3, *shape, *t.stride())
     if n < 1 or n > 4:
         raise SafeditError(ERR_SHAPE, "a tensor of 1 to 4 dims is wanted")
     pad = (0,) * (4 - n)
-    return _TENSOR.pack(t.data_ptr(), _DTYPE[t.dtype], n, *t.shape, *pad, *t.stride(), *pad)
+    return _pack4(t.data_ptr(), code, n, *shape, *pad, *t.stride(), *pad)
 
 
 def _packed_all(ts, device):
