@@ -8,17 +8,30 @@ namespace sd {
 
 // ------------------------------------------------------------- few rows
 // One CTA: 16 query rows (one warp-level matrix tile) of a (b, h) slice and a
-// range of the keys, its warps taking groups of 16 keys in turn.  Bound by
-// reading the state once.  Codes go from global memory into the registers of
-// the warp-level multiplication with no shared memory between: the order of a
+// range of the keys.  Bound by reading the state once: a producer warp keeps a
+// ring of TMA copies of 64 keys' codes of K and V in flight, and four warps
+// take 16 keys each of a stage.  Codes go from shared memory into the
+// registers of the warp-level multiplication as they lie: the order of a
 // row's elements inside the product is free as long as both operands agree,
-// so each lane loads runs of 16 (8, 4) consecutive bytes and hands them out
-// as if they were the tile's scattered elements.
+// so each lane loads runs of consecutive bytes and hands them out as if they
+// were the tile's scattered elements.
 //   scores: lane (g = lane / 4, t = lane % 4) loads bytes [t D/4, (t+1) D/4) of
-//     keys 4 (g / 2) + g % 2 and two further; step s multiplies bytes 4 s..+3.
-//   values: it loads, of keys 4 t..4 t + 3 (whose weights it holds), the
-//     elements of column group g, and interleaves them by bytes.
-constexpr int kRowWarps = 4;
+//     keys g and g + 8; step s multiplies bytes 4 s .. 4 s + 3.
+//   values: it loads, of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (whose weights it
+//     holds), the elements of column group g, and interleaves them by bytes.
+// The copies' 128-byte (d = 128) or 64-byte (d = 64) swizzle keeps those reads
+// off each other's banks; rows of 96 bytes are so by themselves.
+constexpr int kRowWarps = 4;                         // warps that multiply
+constexpr int kRowThreads8 = kRowWarps * 32 + 32;    // and the producer
+constexpr int kStageKeys = 16 * kRowWarps;
+template <int D>
+struct RowsCfg {
+  static constexpr int TILE = kStageKeys * D;        // codes of K (or V) of a stage
+  static constexpr int NST = D == 128 ? 6 : 8;       // stages
+  static constexpr int CTAS = D == 128 ? 2 : (D == 96 ? 2 : 3);  // on an SM
+  static constexpr int SMEM = 1024 + NST * 2 * TILE;
+};
+constexpr uint64_t kRowsDrainNs = 1000000000ull;
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -34,240 +47,277 @@ __device__ __forceinline__ constexpr int value_col(int g, int i) {
   else return g * (D / 8) + i;
 }
 
+// Shared-memory offset of byte `col` of row r of a tile.
 template <int D>
-__device__ __forceinline__ void load_key_run(uint32_t (&w)[D / 16], const uint8_t* at) {
-  if constexpr (D == 96) {
-#pragma unroll
-    for (int e = 0; e < 3; ++e) {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(at) + e);
-      w[2 * e] = x.x, w[2 * e + 1] = x.y;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(at) + e);
-      w[4 * e] = x.x, w[4 * e + 1] = x.y, w[4 * e + 2] = x.z, w[4 * e + 3] = x.w;
-    }
-  }
+__device__ __forceinline__ uint32_t code_at(int r, int col) {
+  const uint32_t off = uint32_t(r * D + col);
+  if constexpr (D == 128) return off ^ (((off >> 7) & 7u) << 4);
+  else if constexpr (D == 64) return off ^ (((off >> 7) & 3u) << 4);
+  else return off;
 }
 
-template <int D>
-__device__ __forceinline__ void load_value_run(uint32_t (&w)[D / 32], const uint8_t* row, int g) {
-  if constexpr (D == 128) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + g * 16));
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-  } else {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(row + g * 8));
-    w[0] = x.x, w[1] = x.y;
-    if constexpr (D == 96) w[2] = __ldg(reinterpret_cast<const uint32_t*>(row + 64 + g * 4));
-  }
+__device__ __forceinline__ uint32_t lds_u32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
 }
-
-template <int D>
-struct RowGroup {  // the codes of 16 keys as one lane holds them
-  uint32_t k[2][D / 16];
-  uint32_t v[4][D / 32];
-  float ks, vs;
-  float pad[4];
-};
+__device__ __forceinline__ void lds_u64(uint32_t at, uint32_t& a, uint32_t& b) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(at));
+}
+__device__ __forceinline__ void lds_u128(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(at));
+}
 
 template <int D, bool PAD, bool E4M3>
-__global__ void __launch_bounds__(kRowWarps * 32) attn_state8_rows_kernel(const __grid_constant__ State8Params p) {
+__global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
+    attn_state8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                            const __grid_constant__ State8Params p) {
+  using C = RowsCfg<D>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int NT = D / 8;  // column tiles of the output
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  extern __shared__ uint8_t rows_smem[];
+  __shared__ uint64_t full[C::NST], empty[C::NST];
+  __shared__ int abort_word;
+  __shared__ float sm_m[kRowWarps][16], sm_l[kRowWarps][16], sm_range[kRowWarps][2];
+  __shared__ float sm_o[16][D];
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = blockIdx.x, tile = blockIdx.y, bh = blockIdx.z;
   const int b = bh / p.H, h = bh - b * p.H;
-  const int ng = (p.Nk + 15) >> 4;
-  const int g_lo = int(int64_t(ng) * split / p.n_split), g_hi = int(int64_t(ng) * (split + 1) / p.n_split);
-
-  // ---- query rows g and g + 8 of the tile, f16, in the order of the key runs
-  uint32_t aq[D / 16][4];
-  float undo[2];
-  int my_q[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = tile * 16 + g + 8 * e;
-    my_q[e] = -1;
-    if (r < p.n_rows) {
-      my_q[e] = p.idx ? __ldg(p.idx + r) : r;
-      if (my_q[e] < 0 || my_q[e] >= p.Nq) {
-        set_status(p.status, SAFEDIT_ERR_INDEX);
-        my_q[e] = -1;
-      }
+  const int ns = (p.Nk + kStageKeys - 1) / kStageKeys;  // stages of the whole slice
+  const int s_lo = int(int64_t(ns) * split / p.n_split), s_hi = int(int64_t(ns) * (split + 1) / p.n_split);
+  const uint32_t ring = (smem_u32(rows_smem) + 1023u) & ~1023u;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), kRowWarps);
     }
-    uint32_t raw[D / 8];
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) raw[c] = 0u;
-    if (my_q[e] >= 0) {
-      const uint2* src = reinterpret_cast<const uint2*>(p.q + b * p.q_sb + h * p.q_sh + int64_t(my_q[e]) * p.q_sr +
-                                                        t * (D / 4));
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint2 x = __ldg(src + c);
-        raw[2 * c] = x.x, raw[2 * c + 1] = x.y;
-      }
-    }
-    uint32_t m = 0u;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) m = max(m, max((raw[c] << 16) & 0x7FFF0000u, raw[c] & 0x7FFF0000u));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const float f = query_factor(m, p.scale_log2, undo[e]);
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      aq[s][e] = pack_f16x2(__uint_as_float(raw[2 * s] << 16) * f, __uint_as_float(raw[2 * s] & 0xFFFF0000u) * f);
-      aq[s][e + 2] =
-          pack_f16x2(__uint_as_float(raw[2 * s + 1] << 16) * f, __uint_as_float(raw[2 * s + 1] & 0xFFFF0000u) * f);
-    }
+    abort_word = 0;
+    mbar_fence_init();
   }
+  __syncthreads();
+  const WaitCtl ctl{&abort_word, p.status, p.wait_limit};
 
-  const uint8_t* kb = p.k + b * p.k_sb + h * p.k_sh + t * (D / 4);
-  const uint8_t* vb = p.v + b * p.v_sb + h * p.v_sh;
-  const float* ksb = p.ks + b * p.ks_sb + h * p.ks_sh;
-  const float* vsb = p.vs + b * p.vs_sb + h * p.vs_sh;
-  const float* padb = PAD ? p.pad + b * p.pad_sb : nullptr;
-  const int key_k = 4 * (g >> 1) + (g & 1);  // this lane's first key of a score tile
-
-  // codes past the last key are zero, and so are those of masked keys: what
-  // they hold (NaN codes too) does not reach a product
-  auto fetch = [&](RowGroup<D>& x, int grp) {
-    const int key0 = grp * 16;
-    x.ks = __ldg(ksb + (key0 >> p.block_log2));
-    x.vs = __ldg(vsb + (key0 >> p.block_log2));
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) x.k[e][c] = 0u;
-      if (key0 + key_k + 2 * e < p.Nk) load_key_run<D>(x.k[e], kb + int64_t(key0 + key_k + 2 * e) * p.k_sr);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int key = key0 + 4 * t + e;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) x.v[e][c] = 0u;
-      if (key < p.Nk) load_value_run<D>(x.v[e], vb + int64_t(key) * p.v_sr, g);
-      if constexpr (PAD) x.pad[e] = key < p.Nk ? __ldg(padb + key) : -INFINITY;
-    }
-  };
-
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float lv_lo = INFINITY, lv_hi = -INFINITY;
+  int my_q[2] = {-1, -1};
+  bool ok = true;
   float o[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float lv_lo = INFINITY, lv_hi = -INFINITY;
-  bool bad = false;
 
-  RowGroup<D> next;
-  int grp = g_lo + warp;
-  if (grp < g_hi) fetch(next, grp);
-  for (; grp < g_hi; grp += kRowWarps) {
-    RowGroup<D> x = next;
-    if (grp + kRowWarps < g_hi) fetch(next, grp + kRowWarps);
-    const int key0 = grp * 16;
-    if constexpr (PAD) {  // a group of masked keys alone: its scales may be anything
-      bool live = false;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) live |= x.pad[e] != -INFINITY;
-      if (!__any_sync(0xffffffffu, live)) continue;
+  if (warp == kRowWarps) {
+    // ------------------------------------------------ producer
+    if (lane == 0) {
+      int n = 0;
+      for (int st = s_lo; st < s_hi; ++st, ++n) {
+        const int i = n % C::NST;
+        if (!wait_bounded(smem_u32(&empty[i]), uint32_t(((n / C::NST) & 1) ^ 1), ctl)) break;
+        const uint32_t at = ring + uint32_t(i * 2 * C::TILE);
+        mbar_arrive_expect_tx(smem_u32(&full[i]), 2 * C::TILE);
+        tma_load_4d(at, &tmK, smem_u32(&full[i]), 0, st * kStageKeys, h, b);
+        tma_load_4d(at + uint32_t(C::TILE), &tmV, smem_u32(&full[i]), 0, st * kStageKeys, h, b);
+      }
+      // every copy has landed before the CTA leaves
+      for (int i = n > C::NST ? n - C::NST : 0; i < n; ++i)
+        wait_drain(smem_u32(&full[i % C::NST]), uint32_t((i / C::NST) & 1), kRowsDrainNs);
     }
-    const float lv = __log2f(x.vs);
-    bad |= !(x.ks >= 0.f && x.ks < INFINITY && x.vs > 0.f && x.vs < INFINITY);
-    lv_lo = fminf(lv_lo, lv);
-    lv_hi = fmaxf(lv_hi, lv);
-    float s[2][4];
+  } else {
+    // ---- query rows g and g + 8 of the tile, f16, in the order of the key runs
+    uint32_t aq[D / 16][4];
+    float undo[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      s[e][0] = s[e][1] = s[e][2] = s[e][3] = 0.f;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint32_t w = bias_codes<E4M3>(x.k[e][c]);
-        mma_16816(s[e], aq[c], widen_lo<E4M3>(w), widen_hi<E4M3>(w));
-      }
-    }
-    // weights of rows g and g + 8, keys key0 + 4 t + {0, 1, 2, 3}
-    uint32_t ap[4];
-    bool up = false;
-    float a[2][4];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float f = undo[r] * x.ks;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = key0 + 4 * t + e;
-        const float raw = s[e >> 1][2 * r + (e & 1)];
-        if constexpr (PAD) {
-          a[r][e] = x.pad[e] == -INFINITY ? -INFINITY : fmaf(raw, f, pad_log2(x.pad[e]));
-        } else {
-          a[r][e] = key < p.Nk ? raw * f : -INFINITY;
+      const int r = tile * 16 + g + 8 * e;
+      if (r < p.n_rows) {
+        my_q[e] = p.idx ? __ldg(p.idx + r) : r;
+        if (my_q[e] < 0 || my_q[e] >= p.Nq) {
+          set_status(p.status, SAFEDIT_ERR_INDEX);
+          my_q[e] = -1;
         }
       }
-      const float top = fmaxf(fmaxf(a[r][0], a[r][1]), fmaxf(a[r][2], a[r][3])) + lv;
-      up |= top > m[r] + 8.f;
+      uint32_t raw[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) raw[c] = 0u;
+      if (my_q[e] >= 0) {
+        const uint2* src = reinterpret_cast<const uint2*>(p.q + b * p.q_sb + h * p.q_sh + int64_t(my_q[e]) * p.q_sr +
+                                                          t * (D / 4));
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint2 x = __ldg(src + c);
+          raw[2 * c] = x.x, raw[2 * c + 1] = x.y;
+        }
+      }
+      uint32_t mb = 0u;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) mb = max(mb, max((raw[c] << 16) & 0x7FFF0000u, raw[c] & 0x7FFF0000u));
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+      const float f = query_factor(mb, p.scale_log2, undo[e]);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        aq[s][e] = pack_f16x2(__uint_as_float(raw[2 * s] << 16) * f, __uint_as_float(raw[2 * s] & 0xFFFF0000u) * f);
+        aq[s][e + 2] =
+            pack_f16x2(__uint_as_float(raw[2 * s + 1] << 16) * f, __uint_as_float(raw[2 * s + 1] & 0xFFFF0000u) * f);
+      }
     }
-    if (__any_sync(0xffffffffu, up)) {
+    const float* ksb = p.ks + b * p.ks_sb + h * p.ks_sh;
+    const float* vsb = p.vs + b * p.vs_sb + h * p.vs_sh;
+    const float* padb = PAD ? p.pad + b * p.pad_sb : nullptr;
+    const int last_block = (p.Nk - 1) >> p.block_log2;
+    bool bad = false;
+    // scales and pads of the next stage are fetched a stage ahead
+    float ks_n = 0.f, vs_n = 1.f, pad_n[4] = {0.f, 0.f, 0.f, 0.f};
+    auto fetch = [&](int st) {
+      const int key0 = st * kStageKeys + warp * 16;
+      const int blk = min(key0 >> p.block_log2, last_block);
+      ks_n = __ldg(ksb + blk);
+      vs_n = __ldg(vsb + blk);
+      if constexpr (PAD) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float top = fmaxf(fmaxf(a[r][0], a[r][1]), fmaxf(a[r][2], a[r][3])) + lv;
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (top > m[r]) {
-          const float al = ex2_approx(m[r] - top);  // 0 from m = -inf
-          m[r] = top;
-          l[r] *= al;
+        for (int e = 0; e < 4; ++e) {
+          const int key = key0 + 2 * t + (e & 1) + 8 * (e >> 1);
+          pad_n[e] = key < p.Nk ? __ldg(padb + key) : -INFINITY;
+        }
+      }
+    };
+    if (s_lo < s_hi) fetch(s_lo);
+    for (int st = s_lo, n = 0; st < s_hi; ++st, ++n) {
+      const float ks = ks_n, vs = vs_n;
+      float pad[4];
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            o[i][2 * r] *= al;
-            o[i][2 * r + 1] *= al;
+      for (int e = 0; e < 4; ++e) pad[e] = pad_n[e];
+      if (st + 1 < s_hi) fetch(st + 1);
+      const int i = n % C::NST;
+      if (!wait_warp(smem_u32(&full[i]), uint32_t((n / C::NST) & 1), ctl)) {
+        ok = false;
+        break;
+      }
+      const int key0 = st * kStageKeys + warp * 16;
+      // a group past the end, or of masked keys alone (its scales may be anything)
+      bool live = key0 < p.Nk;
+      if constexpr (PAD)
+        live = __any_sync(0xffffffffu, fmaxf(fmaxf(pad[0], pad[1]), fmaxf(pad[2], pad[3])) != -INFINITY);
+      if (live) {
+        const uint32_t kt = ring + uint32_t(i * 2 * C::TILE), vt = kt + uint32_t(C::TILE);
+        const float lv = __log2f(vs);
+        bad |= !(ks >= 0.f && ks < INFINITY && vs > 0.f && vs < INFINITY);
+        lv_lo = fminf(lv_lo, lv);
+        lv_hi = fmaxf(lv_hi, lv);
+        float s[2][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t w[D / 16];
+          const int r = warp * 16 + g + 8 * e;
+          if constexpr (D == 96) {
+#pragma unroll
+            for (int c = 0; c < 3; ++c) lds_u64(kt + code_at<D>(r, t * 24 + c * 8), w[2 * c], w[2 * c + 1]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              lds_u128(kt + code_at<D>(r, t * (D / 4) + c * 16), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          }
+          s[e][0] = s[e][1] = s[e][2] = s[e][3] = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const uint32_t x = bias_codes<E4M3>(w[c]);
+            mma_16816(s[e], aq[c], widen_lo<E4M3>(x), widen_hi<E4M3>(x));
           }
         }
+        // weights of rows g and g + 8, keys key0 + {2 t, 2 t + 1, 2 t + 8, 2 t + 9}
+        float a[2][4];
+        bool up = false;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float f = undo[r] * ks;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float raw = s[e >> 1][2 * r + (e & 1)];
+            if constexpr (PAD) {
+              a[r][e] = pad[e] == -INFINITY ? -INFINITY : fmaf(raw, f, pad_log2(pad[e]));
+            } else {
+              a[r][e] = raw * f;
+              if (key0 + 16 > p.Nk && key0 + 2 * t + (e & 1) + 8 * (e >> 1) >= p.Nk) a[r][e] = -INFINITY;
+            }
+          }
+          up |= fmaxf(fmaxf(a[r][0], a[r][1]), fmaxf(a[r][2], a[r][3])) + lv > m[r] + 8.f;
+        }
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float top = fmaxf(fmaxf(a[r][0], a[r][1]), fmaxf(a[r][2], a[r][3])) + lv;
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if (top > m[r]) {
+              const float al = ex2_approx(m[r] - top);  // 0 from m = -inf
+              m[r] = top;
+              l[r] *= al;
+#pragma unroll
+              for (int c = 0; c < NT; ++c) {
+                o[c][2 * r] *= al;
+                o[c][2 * r + 1] *= al;
+              }
+            }
+          }
+        }
+        const float inv = ex2_approx(-lv);
+        uint32_t ap[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mm = m[r] == -INFINITY ? 0.f : m[r];
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = ex2_approx((a[r][e] - mm) + lv);
+          l[r] = fmaf((w[0] + w[1]) + (w[2] + w[3]), inv, l[r]);
+          ap[r] = pack_f16x2(w[0], w[1]);
+          ap[r + 2] = pack_f16x2(w[2], w[3]);
+        }
+        uint32_t w[4][D / 32];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = warp * 16 + 2 * t + (e & 1) + 8 * (e >> 1);
+          if constexpr (D == 128) {
+            lds_u128(vt + code_at<D>(r, g * 16), w[e][0], w[e][1], w[e][2], w[e][3]);
+          } else {
+            lds_u64(vt + code_at<D>(r, g * 8), w[e][0], w[e][1]);
+            if constexpr (D == 96) w[e][2] = lds_u32(vt + code_at<D>(r, 64 + g * 4));
+          }
+          if constexpr (PAD) {  // masked keys: zeros, whatever the codes (NaN) are
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+              if (pad[e] == -INFINITY) w[e][c] = 0u;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = bias_codes<E4M3>(w[e][c]);
+          // bytes of keys (0, 1) and (2, 3) side by side, column by column
+          const uint32_t a0 = __byte_perm(x[0], x[1], 0x5140), a1 = __byte_perm(x[0], x[1], 0x7362);
+          const uint32_t b0 = __byte_perm(x[2], x[3], 0x5140), b1 = __byte_perm(x[2], x[3], 0x7362);
+          mma_16816(o[4 * c], ap, widen_lo<E4M3>(a0), widen_lo<E4M3>(b0));
+          mma_16816(o[4 * c + 1], ap, widen_hi<E4M3>(a0), widen_hi<E4M3>(b0));
+          mma_16816(o[4 * c + 2], ap, widen_lo<E4M3>(a1), widen_lo<E4M3>(b1));
+          mma_16816(o[4 * c + 3], ap, widen_hi<E4M3>(a1), widen_hi<E4M3>(b1));
+        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&empty[i]));
     }
-    const float inv = ex2_approx(-lv);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float mm = m[r] == -INFINITY ? 0.f : m[r];
-      float w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = ex2_approx((a[r][e] - mm) + lv);
-      l[r] = fmaf((w[0] + w[1]) + (w[2] + w[3]), inv, l[r]);
-      ap[r] = pack_f16x2(w[0], w[1]);
-      ap[r + 2] = pack_f16x2(w[2], w[3]);
-    }
-    if constexpr (PAD) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-          if (x.pad[e] == -INFINITY) x.v[e][c] = 0u;
-    }
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = bias_codes<E4M3>(x.v[e][c]);
-      // bytes of keys (0, 1) and (2, 3) side by side, column by column
-      const uint32_t a0 = __byte_perm(w[0], w[1], 0x5140), a1 = __byte_perm(w[0], w[1], 0x7362);
-      const uint32_t b0 = __byte_perm(w[2], w[3], 0x5140), b1 = __byte_perm(w[2], w[3], 0x7362);
-      mma_16816(o[4 * c], ap, widen_lo<E4M3>(a0), widen_lo<E4M3>(b0));
-      mma_16816(o[4 * c + 1], ap, widen_hi<E4M3>(a0), widen_hi<E4M3>(b0));
-      mma_16816(o[4 * c + 2], ap, widen_lo<E4M3>(a1), widen_lo<E4M3>(b1));
-      mma_16816(o[4 * c + 3], ap, widen_hi<E4M3>(a1), widen_hi<E4M3>(b1));
-    }
+    if (bad) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
   }
+  if (__syncthreads_or(!ok)) return;  // a wait ran out: reported, nothing is written
 
   // ---- the warps' results joined in shared memory
-  __shared__ float sm_m[kRowWarps][16], sm_l[kRowWarps][16], sm_range[kRowWarps][2];
-  __shared__ float sm_o[16][D];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    if (t == 0) sm_m[warp][g + 8 * r] = m[r], sm_l[warp][g + 8 * r] = l[r];
+    if (t == 0 && warp < kRowWarps) sm_m[warp][g + 8 * r] = m[r], sm_l[warp][g + 8 * r] = l[r];
   }
-  if (lane == 0) sm_range[warp][0] = lv_lo, sm_range[warp][1] = lv_hi;
-  if (bad) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
-  for (int e = threadIdx.x; e < 16 * D; e += kRowWarps * 32) (&sm_o[0][0])[e] = 0.f;
+  if (lane == 0 && warp < kRowWarps) sm_range[warp][0] = lv_lo, sm_range[warp][1] = lv_hi;
+  for (int e = threadIdx.x; e < 16 * D; e += kRowThreads8) (&sm_o[0][0])[e] = 0.f;
   __syncthreads();
   float mx[2], lx[2];
 #pragma unroll
@@ -297,7 +347,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) attn_state8_rows_kernel(const 
   const int64_t rec = (int64_t(bh) * p.n_tiles + tile) * p.n_split + split;
   if (p.n_split > 1) {
     const PartView pv = part_view(p, rec, D);
-    for (int e = threadIdx.x; e < p.tile_rows * D; e += kRowWarps * 32) pv.o[e] = (&sm_o[0][0])[e];
+    for (int e = threadIdx.x; e < p.tile_rows * D; e += kRowThreads8) pv.o[e] = (&sm_o[0][0])[e];
     if (warp == 0 && t == 0) {
 #pragma unroll
       for (int r = 0; r < 2; ++r)
@@ -312,7 +362,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) attn_state8_rows_kernel(const 
     for (int r = 0; r < 2; ++r) sm_l[0][g + 8 * r] = lx[r], sm_m[0][g + 8 * r] = __int_as_float(my_q[r]);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < 16 * D / 2; e += kRowWarps * 32) {
+  for (int e = threadIdx.x; e < 16 * D / 2; e += kRowThreads8) {
     const int rr = e / (D / 2), c = (e - rr * (D / 2)) * 2;
     const int qi = __float_as_int(sm_m[0][rr]);
     if (qi < 0) continue;
@@ -391,9 +441,9 @@ static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int
   const int64_t units = pl.n_tiles * BH;
   if (units == 0) return pl;
   if (!pl.tc) {
-    // three CTAs on an SM, each warp at least two groups of 16 keys
-    int64_t split = int64_t(sms) * 3 / units;
-    const int64_t most = (Nk + 16 * kRowWarps * 2 - 1) / (16 * kRowWarps * 2);
+    // one wave of what an SM holds, each part two stages of keys at least
+    int64_t split = int64_t(sms) * (D == 64 ? RowsCfg<64>::CTAS : RowsCfg<96>::CTAS) / units;
+    const int64_t most = (Nk + 2 * kStageKeys - 1) / (2 * kStageKeys);
     if (split > most) split = most;
     pl.n_split = split > 1 ? int(split) : 1;
     pl.n_parts = split > 1 ? units : 0;
@@ -435,13 +485,24 @@ static safedit_status launch_join(const State8Params& p, int64_t n_parts, cudaSt
   return after_launch(1);
 }
 
-template <int D, bool PAD>
-static safedit_status launch_rows(const State8Params& p, int64_t BH, bool e4m3, cudaStream_t s) {
+static safedit_status codes_map(CUtensorMap* m, const safedit_tensor* t) {
+  const uint64_t dims[4] = {uint64_t(t->dims[3]), uint64_t(t->dims[2]), uint64_t(t->dims[1]), uint64_t(t->dims[0])};
+  const uint64_t strides[3] = {uint64_t(t->strides[2]), uint64_t(t->strides[1]), uint64_t(t->strides[0])};
+  const uint32_t box[4] = {uint32_t(t->dims[3]), uint32_t(kStageKeys), 1u, 1u};
+  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, t->data, dims, strides, box,
+                     t->dims[3] == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                     : t->dims[3] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                        : CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <int D, bool PAD, bool E4M3>
+static safedit_status launch_rows(const CUtensorMap& tmK, const CUtensorMap& tmV, const State8Params& p, int64_t BH,
+                                  cudaStream_t s) {
+  auto kern = attn_state8_rows_kernel<D, PAD, E4M3>;
+  const safedit_status st = set_smem(reinterpret_cast<const void*>(kern), RowsCfg<D>::SMEM);
+  if (st != SAFEDIT_OK) return st;
   const dim3 grid{unsigned(p.n_split), unsigned(p.n_tiles), unsigned(BH)};
-  if (e4m3)
-    attn_state8_rows_kernel<D, PAD, true><<<grid, kRowWarps * 32, 0, s>>>(p);
-  else
-    attn_state8_rows_kernel<D, PAD, false><<<grid, kRowWarps * 32, 0, s>>>(p);
+  kern<<<grid, kRowThreads8, RowsCfg<D>::SMEM, s>>>(tmK, tmV, p);
   return after_launch(1);
 }
 
@@ -449,12 +510,18 @@ template <int D>
 static safedit_status dispatch_state8(const safedit_tensor* k8, const safedit_tensor* v8, const State8Params& p,
                                       const State8Plan& pl, int64_t BH, cudaStream_t s) {
   safedit_status st;
-  if (pl.tc)
+  if (pl.tc) {
     st = launch_state8_tc(k8, v8, p, pl.n_full + pl.n_parts * pl.n_split, s);
-  else if (p.pad)
-    st = launch_rows<D, true>(p, BH, k8->dtype == SAFEDIT_E4M3, s);
-  else
-    st = launch_rows<D, false>(p, BH, k8->dtype == SAFEDIT_E4M3, s);
+  } else {
+    CUtensorMap tmK, tmV;
+    if ((st = codes_map(&tmK, k8)) != SAFEDIT_OK) return st;
+    if ((st = codes_map(&tmV, v8)) != SAFEDIT_OK) return st;
+    const bool e4m3 = k8->dtype == SAFEDIT_E4M3;
+    if (p.pad)
+      st = e4m3 ? launch_rows<D, true, true>(tmK, tmV, p, BH, s) : launch_rows<D, true, false>(tmK, tmV, p, BH, s);
+    else
+      st = e4m3 ? launch_rows<D, false, true>(tmK, tmV, p, BH, s) : launch_rows<D, false, false>(tmK, tmV, p, BH, s);
+  }
   if (st != SAFEDIT_OK || pl.n_parts == 0) return st;
   return launch_join<D>(p, pl.n_parts, s);
 }

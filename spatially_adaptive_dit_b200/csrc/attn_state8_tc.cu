@@ -556,9 +556,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sts128(a1, o[4], o[5], o[6], o[7]);
     };
     // masked keys: zeros, whatever the codes (NaN) are
-    auto clear_dead = [&](uint4& v, int key) {
+    auto clear_dead = [&](uint4& v, uint32_t pads, int r) {
       if constexpr (PAD) {
-        if (key < p.Nk && __ldg(padb + key) == -INFINITY) v = make_uint4(0u, 0u, 0u, 0u);
+        if (lds32(pads + uint32_t(r * 4)) == -INFINITY) v = make_uint4(0u, 0u, 0u, 0u);
       }
     };
     constexpr int RPP = kTcWidenThreads / UPR;  // d = 64, 128: rows a pass
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t p0 = chunk0 + tc_swizzle(in_row + (swap ? 16u : 0u), C::LAYOUT);
     const uint32_t p1 = chunk0 + tc_swizzle(in_row + (swap ? 0u : 16u), C::LAYOUT);
     // the loads of four units go out before the first is widened
-    auto widen = [&](uint32_t raw, uint32_t to, int key0) {
+    auto widen = [&](uint32_t raw, uint32_t to, uint32_t pads) {
       if constexpr (D == 96) {
 #pragma unroll
         for (int i0 = 0; i0 < 8; i0 += 4) {
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int i = 0; i < 4; ++i) {
             const int r = i0 + i < 6 ? tid : 96 + lane, c = i0 + i < 6 ? i0 + i : (tid >> 5) * 2 + i0 + i - 6;
             v[i] = lds128(raw + uint32_t(r * D + c * 16));
-            clear_dead(v[i], key0 + r);
+            clear_dead(v[i], pads, r);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int i = i0; i < i0 + 4 && i < PASSES; ++i) {
             if (i + 1 < PASSES || u_row + i * RPP < 128) {
               v[i - i0] = lds128(raw + uint32_t(tid * 16 + i * RPP * D));
-              clear_dead(v[i - i0], key0 + u_row + i * RPP);
+              clear_dead(v[i - i0], pads, u_row + i * RPP);
             }
           }
 #pragma unroll
@@ -626,62 +626,89 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     if (tid == 0)
       for (int n = 0; n < C::NR; ++n) load_next();
+    // Scale factors and pads of a key tile, in NS + 1 slots, published a tile
+    // ahead: with the V tile of tile `it`, when V tile `it - NS` is free.  Its
+    // products took the weights of tile `it - NS` from both query tiles, so
+    // nobody reads that slot any more, and tile `it + 1` takes it.  Their loads
+    // go out a step before.
+    float next_ks = 0.f, next_vs = 1.f, next_pad[2] = {0.f, 0.f};
+    auto fetch = [&](int kt) {
+      const int key = kt * C::BN + tid * 16;
+      if (tid < 8 && key < p.Nk) {
+        next_ks = __ldg(ksb + (key >> p.block_log2));
+        next_vs = __ldg(vsb + (key >> p.block_log2));
+      }
+      if constexpr (PAD) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = tid + e * kTcWidenThreads, k = kt * C::BN + c;
+          if (c < C::BN) next_pad[e] = k < p.Nk ? __ldg(padb + k) : -INFINITY;
+        }
+      }
+    };
+    auto publish = [&](int kt, int slot) {
+      if (tid < 8) {
+        const int key = kt * C::BN + tid * 16;
+        float ks = 0.f, lv = 0.f;
+        if (key < p.Nk) {
+          ks = next_ks;
+          lv = __log2f(next_vs);
+          if (!(ks >= 0.f && ks < INFINITY && next_vs > 0.f && next_vs < INFINITY)) {
+            bool used = true;  // a key of the group that is not masked
+            if constexpr (PAD) {
+              used = false;
+              for (int e = 0; e < 16 && key + e < p.Nk; ++e) used |= __ldg(padb + key + e) != -INFINITY;
+            }
+            if (used) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
+            else ks = 0.f, lv = 0.f;
+          } else {
+            lv_lo = fminf(lv_lo, lv);
+            lv_hi = fmaxf(lv_hi, lv);
+          }
+        }
+        const uint32_t f = sb + uint32_t(C::OFF_FACT + slot * 96 + tid * 4);
+        sts32(f, ks);
+        sts32(f + 32u, lv);
+        sts32(f + 64u, ex2_approx(-lv));
+      }
+      if constexpr (PAD) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = tid + e * kTcWidenThreads;
+          if (c < C::BN) sts32(sb + uint32_t(C::OFF_PAD + slot * 512 + c * 4), pad_log2(next_pad[e]));
+        }
+      }
+    };
     bool ok = true;
-    int slot = 0;
-    for (int it = 0, kt = next_live(k_lo); ok && it < n_live; ++it, kt = next_live(kt + 1)) {
+    int slot = 0, kt = next_live(k_lo);
+    if (n_live > 0) {
+      fetch(kt);
+      publish(kt, 0);
+    }
+    bar_any(1, kTcWidenThreads, false);
+    for (int it = 0; ok && it < n_live; ++it) {
       const int s = it % C::NS;
       const uint32_t ph = uint32_t((it / C::NS) & 1) ^ 1u;
-      const int key0 = kt * C::BN;
+      const int kt1 = next_live(kt + 1), slot1 = slot + 1 == C::NF ? 0 : slot + 1;
+      const bool more = it + 1 < n_live;
+      if (more) fetch(kt1);
       for (int kv = 0; ok && kv < 2; ++kv) {
         const int n = 2 * it + kv, raw = n % C::NR;
         ok = wait_warp(BAR(RAW_FULL + raw), uint32_t((n / C::NR) & 1), ctl) &&
              wait_warp(BAR((kv ? V_EMPTY : K_EMPTY) + s), ph, ctl);
-        if (ok && kv == 0) {
-          // Scale factors and pads of the tile, NS + 1 slots: when the K tile
-          // `it - NS` is free, its scores are done, which took the weights of
-          // tile `it - NS - 1` from both query tiles, so nobody reads a slot
-          // older than `it - NS`.
-          if (tid < 8) {
-            const int key = key0 + tid * 16;
-            float ks = 0.f, lv = 0.f;
-            if (key < p.Nk) {
-              ks = __ldg(ksb + (key >> p.block_log2));
-              const float vs = __ldg(vsb + (key >> p.block_log2));
-              lv = __log2f(vs);
-              if (!(ks >= 0.f && ks < INFINITY && vs > 0.f && vs < INFINITY)) {
-                bool used = true;  // a key of the group that is not masked
-                if constexpr (PAD) {
-                  used = false;
-                  for (int e = 0; e < 16 && key + e < p.Nk; ++e) used |= __ldg(padb + key + e) != -INFINITY;
-                }
-                if (used) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
-                else ks = 0.f, lv = 0.f;
-              } else {
-                lv_lo = fminf(lv_lo, lv);
-                lv_hi = fmaxf(lv_hi, lv);
-              }
-            }
-            const uint32_t f = sb + uint32_t(C::OFF_FACT + slot * 96 + tid * 4);
-            sts32(f, ks);
-            sts32(f + 32u, lv);
-            sts32(f + 64u, ex2_approx(-lv));
-          }
-          if constexpr (PAD) {
-            for (int e = tid; e < C::BN; e += kTcWidenThreads)
-              sts32(sb + uint32_t(C::OFF_PAD + slot * 512 + e * 4),
-                    key0 + e < p.Nk ? pad_log2(__ldg(padb + key0 + e)) : -INFINITY);
-          }
-        }
         if (ok) {
+          if (kv && more) publish(kt1, slot1);
           widen(sb + uint32_t(C::OFF_RAW + raw * C::RAW_BYTES),
-                sb + uint32_t((kv ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES), key0);
+                sb + uint32_t((kv ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES),
+                sb + uint32_t(C::OFF_PAD + slot * 512));
           fence_proxy_async_smem();
           warp_arrive(BAR((kv ? V_FULL : K_FULL) + s), lane);
         }
         ok = !bar_any(1, kTcWidenThreads, !ok);  // read by all three warps, or given up by all
         if (ok && tid == 0) load_next();
       }
-      slot = slot + 1 == C::NF ? 0 : slot + 1;
+      kt = kt1;
+      slot = slot1;
     }
     // every copy has landed before the CTA leaves
     if (tid == 0)
