@@ -7,18 +7,22 @@
 namespace sd {
 
 // ------------------------------------------------------------- few rows
-// One CTA: 16 query rows (one warp-level matrix tile) of a (b, h) slice and a
-// range of the keys.  Bound by reading the state once: a producer warp keeps a
+// One CTA: 8 or 16 query rows of a (b, h) slice and a range of the keys.  Bound by reading the state once: a producer warp keeps a
 // ring of TMA copies of 64 keys' codes of K and V in flight, and four warps
 // take 16 keys each of a stage.  Codes go from shared memory into the
 // registers of the warp-level multiplication as they lie: the order of a
 // row's elements inside the product is free as long as both operands agree,
 // so each lane loads runs of consecutive bytes and hands them out as if they
 // were the tile's scattered elements.
-//   scores: lane (g = lane / 4, t = lane % 4) loads bytes [t D/4, (t+1) D/4) of
-//     keys g and g + 8; step s multiplies bytes 4 s .. 4 s + 3.
-//   values: it loads, of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (whose weights it
-//     holds), the elements of column group g, and interleaves them by bytes.
+// Keys are the rows of both products and queries the columns, eight to a tile
+// (NQ = 1 or 2 tiles), so a single query wastes an eighth of what it would as
+// one of 16 rows:
+//   scores^T = K Q^T: lane (g = lane / 4, t = lane % 4) loads bytes
+//     [t D/4, (t+1) D/4) of keys g and g + 8; step s multiplies bytes 4 s..+3.
+//     It then holds keys g, g + 8 of queries 2 t, 2 t + 1;
+//   out^T = V^T W^T: the weights' 8 x 8 blocks are transposed between the
+//     lanes; the lane loads, of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, the
+//     elements of column group g, and interleaves them by bytes.
 // The copies' 128-byte (d = 128) or 64-byte (d = 64) swizzle keeps those reads
 // off each other's banks; rows of 96 bytes are so by themselves.
 constexpr int kRowWarps = 4;                         // warps that multiply
@@ -27,8 +31,8 @@ constexpr int kStageKeys = 16 * kRowWarps;
 template <int D>
 struct RowsCfg {
   static constexpr int TILE = kStageKeys * D;        // codes of K (or V) of a stage
-  static constexpr int NST = D == 128 ? 6 : 8;       // stages
-  static constexpr int CTAS = D == 128 ? 2 : (D == 96 ? 2 : 3);  // on an SM
+  static constexpr int NST = D == 128 ? 4 : (D == 96 ? 5 : 6);  // stages
+  static constexpr int CTAS = D == 64 ? 4 : 3;       // on an SM
   static constexpr int SMEM = 1024 + NST * 2 * TILE;
 };
 constexpr uint64_t kRowsDrainNs = 1000000000ull;
@@ -68,18 +72,26 @@ __device__ __forceinline__ void lds_u128(uint32_t at, uint32_t& a, uint32_t& b, 
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(at));
 }
 
-template <int D, bool PAD, bool E4M3>
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <int D, int NQ, bool PAD, bool E4M3>
 __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
     attn_state8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const __grid_constant__ State8Params p) {
   using C = RowsCfg<D>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int NT = D / 8;  // column tiles of the output
+  constexpr int NT = D / 16;       // tiles of 16 output columns
+  constexpr int ROWS = 8 * NQ;     // query rows of the CTA
+  constexpr bool CLEAR = PAD && E4M3;  // codes of masked keys may be NaN
   extern __shared__ uint8_t rows_smem[];
   __shared__ uint64_t full[C::NST], empty[C::NST];
   __shared__ int abort_word;
-  __shared__ float sm_m[kRowWarps][16], sm_l[kRowWarps][16], sm_range[kRowWarps][2];
-  __shared__ float sm_o[16][D];
+  __shared__ float sm_m[kRowWarps][ROWS], sm_l[kRowWarps][ROWS], sm_range[kRowWarps][2];
+  __shared__ float sm_o[ROWS][D];
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = blockIdx.x, tile = blockIdx.y, bh = blockIdx.z;
@@ -98,13 +110,18 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   __syncthreads();
   const WaitCtl ctl{&abort_word, p.status, p.wait_limit};
 
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // queries 2 t and 2 t + 1 of each tile of eight
+  float m[NQ][2], l[NQ][2];
   float lv_lo = INFINITY, lv_hi = -INFINITY;
-  int my_q[2] = {-1, -1};
   bool ok = true;
-  float o[NT][4];
+  float o[NQ][NT][4];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  for (int q = 0; q < NQ; ++q) {
+    m[q][0] = m[q][1] = -INFINITY;
+    l[q][0] = l[q][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[q][i][0] = o[q][i][1] = o[q][i][2] = o[q][i][3] = 0.f;
+  }
 
   if (warp == kRowWarps) {
     // ------------------------------------------------ producer
@@ -123,25 +140,26 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
         wait_drain(smem_u32(&full[i % C::NST]), uint32_t((i / C::NST) & 1), kRowsDrainNs);
     }
   } else {
-    // ---- query rows g and g + 8 of the tile, f16, in the order of the key runs
-    uint32_t aq[D / 16][4];
-    float undo[2];
+    // ---- query row g of each tile of eight, f16, in the order of the key runs
+    uint32_t bq[NQ][D / 16][2];
+    float undo[NQ][2];  // of queries 2 t and 2 t + 1
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = tile * 16 + g + 8 * e;
+    for (int q = 0; q < NQ; ++q) {
+      const int r = tile * ROWS + 8 * q + g;
+      int qi = -1;
       if (r < p.n_rows) {
-        my_q[e] = p.idx ? __ldg(p.idx + r) : r;
-        if (my_q[e] < 0 || my_q[e] >= p.Nq) {
+        qi = p.idx ? __ldg(p.idx + r) : r;
+        if (qi < 0 || qi >= p.Nq) {
           set_status(p.status, SAFEDIT_ERR_INDEX);
-          my_q[e] = -1;
+          qi = -1;
         }
       }
       uint32_t raw[D / 8];
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) raw[c] = 0u;
-      if (my_q[e] >= 0) {
-        const uint2* src = reinterpret_cast<const uint2*>(p.q + b * p.q_sb + h * p.q_sh + int64_t(my_q[e]) * p.q_sr +
-                                                          t * (D / 4));
+      if (qi >= 0) {
+        const uint2* src =
+            reinterpret_cast<const uint2*>(p.q + b * p.q_sb + h * p.q_sh + int64_t(qi) * p.q_sr + t * (D / 4));
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           const uint2 x = __ldg(src + c);
@@ -153,11 +171,14 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
       for (int c = 0; c < D / 8; ++c) mb = max(mb, max((raw[c] << 16) & 0x7FFF0000u, raw[c] & 0x7FFF0000u));
       mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
       mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
-      const float f = query_factor(mb, p.scale_log2, undo[e]);
+      float un;
+      const float f = query_factor(mb, p.scale_log2, un);
+      undo[q][0] = __shfl_sync(0xffffffffu, un, 8 * t);
+      undo[q][1] = __shfl_sync(0xffffffffu, un, 8 * t + 4);
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
-        aq[s][e] = pack_f16x2(__uint_as_float(raw[2 * s] << 16) * f, __uint_as_float(raw[2 * s] & 0xFFFF0000u) * f);
-        aq[s][e + 2] =
+        bq[q][s][0] = pack_f16x2(__uint_as_float(raw[2 * s] << 16) * f, __uint_as_float(raw[2 * s] & 0xFFFF0000u) * f);
+        bq[q][s][1] =
             pack_f16x2(__uint_as_float(raw[2 * s + 1] << 16) * f, __uint_as_float(raw[2 * s + 1] & 0xFFFF0000u) * f);
       }
     }
@@ -166,27 +187,27 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
     const float* padb = PAD ? p.pad + b * p.pad_sb : nullptr;
     const int last_block = (p.Nk - 1) >> p.block_log2;
     bool bad = false;
-    // scales and pads of the next stage are fetched a stage ahead
-    float ks_n = 0.f, vs_n = 1.f, pad_n[4] = {0.f, 0.f, 0.f, 0.f};
+    // scales and pads of the next stage are fetched a stage ahead: pads of keys
+    // g, g + 8 and, where codes have to be cleared, 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+    float ks_n = 0.f, vs_n = 1.f, pad_n[2] = {0.f, 0.f}, padv_n[4] = {0.f, 0.f, 0.f, 0.f};
+    auto pad_of = [&](int key) { return key < p.Nk ? __ldg(padb + key) : -INFINITY; };
     auto fetch = [&](int st) {
       const int key0 = st * kStageKeys + warp * 16;
       const int blk = min(key0 >> p.block_log2, last_block);
       ks_n = __ldg(ksb + blk);
       vs_n = __ldg(vsb + blk);
       if constexpr (PAD) {
+        pad_n[0] = pad_of(key0 + g), pad_n[1] = pad_of(key0 + g + 8);
+        if constexpr (CLEAR) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = key0 + 2 * t + (e & 1) + 8 * (e >> 1);
-          pad_n[e] = key < p.Nk ? __ldg(padb + key) : -INFINITY;
+          for (int e = 0; e < 4; ++e) padv_n[e] = pad_of(key0 + 2 * t + (e & 1) + 8 * (e >> 1));
         }
       }
     };
     if (s_lo < s_hi) fetch(s_lo);
     for (int st = s_lo, n = 0; st < s_hi; ++st, ++n) {
-      const float ks = ks_n, vs = vs_n;
-      float pad[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) pad[e] = pad_n[e];
+      const float ks = ks_n, vs = vs_n, pad[2] = {pad_n[0], pad_n[1]};
+      const float padv[4] = {padv_n[0], padv_n[1], padv_n[2], padv_n[3]};
       if (st + 1 < s_hi) fetch(st + 1);
       const int i = n % C::NST;
       if (!wait_warp(smem_u32(&full[i]), uint32_t((n / C::NST) & 1), ctl)) {
@@ -196,81 +217,95 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
       const int key0 = st * kStageKeys + warp * 16;
       // a group past the end, or of masked keys alone (its scales may be anything)
       bool live = key0 < p.Nk;
-      if constexpr (PAD)
-        live = __any_sync(0xffffffffu, fmaxf(fmaxf(pad[0], pad[1]), fmaxf(pad[2], pad[3])) != -INFINITY);
+      if constexpr (PAD) live = __any_sync(0xffffffffu, pad[0] != -INFINITY || pad[1] != -INFINITY);
       if (live) {
         const uint32_t kt = ring + uint32_t(i * 2 * C::TILE), vt = kt + uint32_t(C::TILE);
         const float lv = __log2f(vs);
-        bad |= !(ks >= 0.f && ks < INFINITY && vs > 0.f && vs < INFINITY);
+        // finite, ks >= 0, vs > 0, by their bits
+        bad |= __float_as_uint(ks) >= 0x7F800000u || __float_as_uint(vs) - 1u >= 0x7F7FFFFFu;
         lv_lo = fminf(lv_lo, lv);
         lv_hi = fmaxf(lv_hi, lv);
-        float s[2][4];
+        float s[NQ][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t w[D / 16];
-          const int r = warp * 16 + g + 8 * e;
-          if constexpr (D == 96) {
+        for (int q = 0; q < NQ; ++q) s[q][0] = s[q][1] = s[q][2] = s[q][3] = 0.f;
+        {
+          uint32_t w[2][D / 16];
 #pragma unroll
-            for (int c = 0; c < 3; ++c) lds_u64(kt + code_at<D>(r, t * 24 + c * 8), w[2 * c], w[2 * c + 1]);
-          } else {
+          for (int e = 0; e < 2; ++e) {
+            const int r = warp * 16 + g + 8 * e;
+            if constexpr (D == 96) {
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              lds_u128(kt + code_at<D>(r, t * (D / 4) + c * 16), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-          }
-          s[e][0] = s[e][1] = s[e][2] = s[e][3] = 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const uint32_t x = bias_codes<E4M3>(w[c]);
-            mma_16816(s[e], aq[c], widen_lo<E4M3>(x), widen_hi<E4M3>(x));
-          }
-        }
-        // weights of rows g and g + 8, keys key0 + {2 t, 2 t + 1, 2 t + 8, 2 t + 9}
-        float a[2][4];
-        bool up = false;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float f = undo[r] * ks;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float raw = s[e >> 1][2 * r + (e & 1)];
-            if constexpr (PAD) {
-              a[r][e] = pad[e] == -INFINITY ? -INFINITY : fmaf(raw, f, pad_log2(pad[e]));
+              for (int c = 0; c < 3; ++c) lds_u64(kt + code_at<D>(r, t * 24 + c * 8), w[e][2 * c], w[e][2 * c + 1]);
             } else {
-              a[r][e] = raw * f;
-              if (key0 + 16 > p.Nk && key0 + 2 * t + (e & 1) + 8 * (e >> 1) >= p.Nk) a[r][e] = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                lds_u128(kt + code_at<D>(r, t * (D / 4) + c * 16), w[e][4 * c], w[e][4 * c + 1], w[e][4 * c + 2],
+                         w[e][4 * c + 3]);
             }
           }
-          up |= fmaxf(fmaxf(a[r][0], a[r][1]), fmaxf(a[r][2], a[r][3])) + lv > m[r] + 8.f;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const uint32_t x0 = bias_codes<E4M3>(w[0][c]), x1 = bias_codes<E4M3>(w[1][c]);
+            const uint32_t a[4] = {widen_lo<E4M3>(x0), widen_lo<E4M3>(x1), widen_hi<E4M3>(x0), widen_hi<E4M3>(x1)};
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) mma_16816(s[q], a, bq[q][c][0], bq[q][c][1]);
+          }
+        }
+        // exponents against the queries' references; element e: key g + 8 (e / 2),
+        // query 2 t + e % 2
+        bool up = false;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f = undo[q][e & 1] * ks;
+            if constexpr (PAD)
+              s[q][e] = pad[e >> 1] == -INFINITY ? -INFINITY : fmaf(s[q][e], f, pad_log2(pad[e >> 1]));
+            else
+              s[q][e] *= f;
+          }
+          if (!PAD && key0 + 16 > p.Nk) {
+            if (key0 + g >= p.Nk) s[q][0] = s[q][1] = -INFINITY;
+            if (key0 + g + 8 >= p.Nk) s[q][2] = s[q][3] = -INFINITY;
+          }
+          up |= fmaxf(s[q][0], s[q][2]) + lv > m[q][0] + 8.f;
+          up |= fmaxf(s[q][1], s[q][3]) + lv > m[q][1] + 8.f;
         }
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float top = fmaxf(fmaxf(a[r][0], a[r][1]), fmaxf(a[r][2], a[r][3])) + lv;
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            if (top > m[r]) {
-              const float al = ex2_approx(m[r] - top);  // 0 from m = -inf
-              m[r] = top;
-              l[r] *= al;
+          for (int q = 0; q < NQ; ++q)
 #pragma unroll
-              for (int c = 0; c < NT; ++c) {
-                o[c][2 * r] *= al;
-                o[c][2 * r + 1] *= al;
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(s[q][e], s[q][e + 2]) + lv;
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              if (top > m[q][e]) {
+                const float al = ex2_approx(m[q][e] - top);  // 0 from m = -inf
+                m[q][e] = top;
+                l[q][e] *= al;
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                  o[q][c][e] *= al;
+                  o[q][c][e + 2] *= al;
+                }
               }
             }
-          }
         }
         const float inv = ex2_approx(-lv);
-        uint32_t ap[4];
+        uint32_t bp[NQ][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float mm = m[r] == -INFINITY ? 0.f : m[r];
+        for (int q = 0; q < NQ; ++q) {
           float w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = ex2_approx((a[r][e] - mm) + lv);
-          l[r] = fmaf((w[0] + w[1]) + (w[2] + w[3]), inv, l[r]);
-          ap[r] = pack_f16x2(w[0], w[1]);
-          ap[r + 2] = pack_f16x2(w[2], w[3]);
+          for (int e = 0; e < 4; ++e) {
+            const float mm = m[q][e & 1] == -INFINITY ? 0.f : m[q][e & 1];
+            w[e] = ex2_approx((s[q][e] - mm) + lv);
+          }
+          l[q][0] = fmaf(w[0] + w[2], inv, l[q][0]);
+          l[q][1] = fmaf(w[1] + w[3], inv, l[q][1]);
+          bp[q][0] = transpose_8x8(pack_f16x2(w[0], w[1]));
+          bp[q][1] = transpose_8x8(pack_f16x2(w[2], w[3]));
         }
         uint32_t w[4][D / 32];
 #pragma unroll
@@ -282,10 +317,10 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
             lds_u64(vt + code_at<D>(r, g * 8), w[e][0], w[e][1]);
             if constexpr (D == 96) w[e][2] = lds_u32(vt + code_at<D>(r, 64 + g * 4));
           }
-          if constexpr (PAD) {  // masked keys: zeros, whatever the codes (NaN) are
+          if constexpr (CLEAR) {
 #pragma unroll
             for (int c = 0; c < D / 32; ++c)
-              if (pad[e] == -INFINITY) w[e][c] = 0u;
+              if (padv[e] == -INFINITY) w[e][c] = 0u;
           }
         }
 #pragma unroll
@@ -294,12 +329,15 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = bias_codes<E4M3>(w[e][c]);
           // bytes of keys (0, 1) and (2, 3) side by side, column by column
-          const uint32_t a0 = __byte_perm(x[0], x[1], 0x5140), a1 = __byte_perm(x[0], x[1], 0x7362);
-          const uint32_t b0 = __byte_perm(x[2], x[3], 0x5140), b1 = __byte_perm(x[2], x[3], 0x7362);
-          mma_16816(o[4 * c], ap, widen_lo<E4M3>(a0), widen_lo<E4M3>(b0));
-          mma_16816(o[4 * c + 1], ap, widen_hi<E4M3>(a0), widen_hi<E4M3>(b0));
-          mma_16816(o[4 * c + 2], ap, widen_lo<E4M3>(a1), widen_lo<E4M3>(b1));
-          mma_16816(o[4 * c + 3], ap, widen_hi<E4M3>(a1), widen_hi<E4M3>(b1));
+          const uint32_t u0 = __byte_perm(x[0], x[1], 0x5140), u1 = __byte_perm(x[0], x[1], 0x7362);
+          const uint32_t v0 = __byte_perm(x[2], x[3], 0x5140), v1 = __byte_perm(x[2], x[3], 0x7362);
+          const uint32_t a0[4] = {widen_lo<E4M3>(u0), widen_hi<E4M3>(u0), widen_lo<E4M3>(v0), widen_hi<E4M3>(v0)};
+          const uint32_t a1[4] = {widen_lo<E4M3>(u1), widen_hi<E4M3>(u1), widen_lo<E4M3>(v1), widen_hi<E4M3>(v1)};
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            mma_16816(o[q][2 * c], a0, bp[q][0], bp[q][1]);
+            mma_16816(o[q][2 * c + 1], a1, bp[q][0], bp[q][1]);
+          }
         }
       }
       __syncwarp();
@@ -310,66 +348,67 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   if (__syncthreads_or(!ok)) return;  // a wait ran out: reported, nothing is written
 
   // ---- the warps' results joined in shared memory
+  if (warp < kRowWarps) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    if (t == 0 && warp < kRowWarps) sm_m[warp][g + 8 * r] = m[r], sm_l[warp][g + 8 * r] = l[r];
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 4);
+        l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 8);
+        l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 16);
+        if (g == 0) sm_m[warp][8 * q + 2 * t + e] = m[q][e], sm_l[warp][8 * q + 2 * t + e] = l[q][e];
+      }
+    if (lane == 0) sm_range[warp][0] = lv_lo, sm_range[warp][1] = lv_hi;
   }
-  if (lane == 0 && warp < kRowWarps) sm_range[warp][0] = lv_lo, sm_range[warp][1] = lv_hi;
-  for (int e = threadIdx.x; e < 16 * D; e += kRowThreads8) (&sm_o[0][0])[e] = 0.f;
+  for (int e = threadIdx.x; e < ROWS * D; e += kRowThreads8) (&sm_o[0][0])[e] = 0.f;
   __syncthreads();
-  float mx[2], lx[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int rr = g + 8 * r;
-    mx[r] = -INFINITY, lx[r] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) mx[r] = fmaxf(mx[r], sm_m[w][rr]);
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w)
-      if (sm_m[w][rr] != -INFINITY) lx[r] = fmaf(ex2_approx(sm_m[w][rr] - mx[r]), sm_l[w][rr], lx[r]);
-    m[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - mx[r]);  // this warp's factor
-  }
   for (int w = 0; w < kRowWarps; ++w) {  // one warp after another: the sum's order is fixed
     if (warp == w) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int q = 0; q < NQ; ++q)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          sm_o[g + 8 * r][value_col<D>(2 * t, i)] += o[i][2 * r] * m[r];
-          sm_o[g + 8 * r][value_col<D>(2 * t + 1, i)] += o[i][2 * r + 1] * m[r];
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * q + 2 * t + e;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int v = 0; v < kRowWarps; ++v) mx = fmaxf(mx, sm_m[v][r]);
+          const float f = m[q][e] == -INFINITY ? 0.f : ex2_approx(m[q][e] - mx);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            sm_o[r][value_col<D>(g, 2 * i)] += o[q][i][e] * f;
+            sm_o[r][value_col<D>(g, 2 * i + 1)] += o[q][i][e + 2] * f;
+          }
         }
     }
     __syncthreads();
   }
   for (int w = 0; w < kRowWarps; ++w) lv_lo = fminf(lv_lo, sm_range[w][0]), lv_hi = fmaxf(lv_hi, sm_range[w][1]);
-  const int64_t rec = (int64_t(bh) * p.n_tiles + tile) * p.n_split + split;
+  float mx = -INFINITY, lx = 0.f;  // of row threadIdx.x
+  if (threadIdx.x < ROWS) {
+    for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, sm_m[w][threadIdx.x]);
+    for (int w = 0; w < kRowWarps; ++w)
+      if (sm_m[w][threadIdx.x] != -INFINITY) lx = fmaf(ex2_approx(sm_m[w][threadIdx.x] - mx), sm_l[w][threadIdx.x], lx);
+  }
   if (p.n_split > 1) {
-    const PartView pv = part_view(p, rec, D);
+    const PartView pv = part_view(p, (int64_t(bh) * p.n_tiles + tile) * p.n_split + split, D);
     for (int e = threadIdx.x; e < p.tile_rows * D; e += kRowThreads8) pv.o[e] = (&sm_o[0][0])[e];
-    if (warp == 0 && t == 0) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-        if (g + 8 * r < p.tile_rows) pv.ml[(g + 8 * r) * 2] = mx[r], pv.ml[(g + 8 * r) * 2 + 1] = lx[r];
-    }
+    if (threadIdx.x < p.tile_rows) pv.ml[threadIdx.x * 2] = mx, pv.ml[threadIdx.x * 2 + 1] = lx;
     if (threadIdx.x == 0) pv.range[0] = lv_lo, pv.range[1] = lv_hi;
     return;
   }
   if (threadIdx.x == 0 && lv_hi - lv_lo > kScaleSpread) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
-  if (warp == 0 && t == 0) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) sm_l[0][g + 8 * r] = lx[r], sm_m[0][g + 8 * r] = __int_as_float(my_q[r]);
-  }
+  __syncthreads();  // every sm_l has been read
+  if (threadIdx.x < ROWS) sm_l[0][threadIdx.x] = lx;
   __syncthreads();
-  for (int e = threadIdx.x; e < 16 * D / 2; e += kRowThreads8) {
-    const int rr = e / (D / 2), c = (e - rr * (D / 2)) * 2;
-    const int qi = __float_as_int(sm_m[0][rr]);
-    if (qi < 0) continue;
+  for (int e = threadIdx.x; e < ROWS * D / 2; e += kRowThreads8) {
+    const int rr = e / (D / 2), c = (e - rr * (D / 2)) * 2, r = tile * ROWS + rr;
+    if (r >= p.n_rows) break;
+    const int qi = p.idx ? __ldg(p.idx + r) : r;
+    if (qi < 0 || qi >= p.Nq) continue;
     const float ls = sm_l[0][rr];
     if (ls == 0.f && c == 0) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
     const float inv = ls == 0.f ? 0.f : 1.f / ls;
-    const int64_t orow = p.out_scattered ? int64_t(qi) : int64_t(tile * 16 + rr);
+    const int64_t orow = p.out_scattered ? int64_t(qi) : int64_t(r);
     *reinterpret_cast<uint32_t*>(p.out + b * p.o_sb + h * p.o_sh + orow * p.o_sr + c) =
         pack_bf16x2(sm_o[rr][c] * inv, sm_o[rr][c + 1] * inv);
   }
@@ -435,14 +474,14 @@ constexpr int64_t kFewRows = 16;
 static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int sms) {
   State8Plan pl;
   pl.tc = n_rows > kFewRows;
-  pl.unit_rows = pl.tc ? 256 : 16;
+  pl.unit_rows = pl.tc ? 256 : (n_rows <= 8 ? 8 : 16);
   pl.tile_rows = n_rows < pl.unit_rows ? int(n_rows) : pl.unit_rows;
   pl.n_tiles = int((n_rows + pl.unit_rows - 1) / pl.unit_rows);
   const int64_t units = pl.n_tiles * BH;
   if (units == 0) return pl;
   if (!pl.tc) {
     // one wave of what an SM holds, each part two stages of keys at least
-    int64_t split = int64_t(sms) * (D == 64 ? RowsCfg<64>::CTAS : RowsCfg<96>::CTAS) / units;
+    int64_t split = int64_t(sms) * (D == 64 ? RowsCfg<64>::CTAS : D == 96 ? RowsCfg<96>::CTAS : RowsCfg<128>::CTAS) / units;
     const int64_t most = (Nk + 2 * kStageKeys - 1) / (2 * kStageKeys);
     if (split > most) split = most;
     pl.n_split = split > 1 ? int(split) : 1;
@@ -498,7 +537,7 @@ static safedit_status codes_map(CUtensorMap* m, const safedit_tensor* t) {
 template <int D, bool PAD, bool E4M3>
 static safedit_status launch_rows(const CUtensorMap& tmK, const CUtensorMap& tmV, const State8Params& p, int64_t BH,
                                   cudaStream_t s) {
-  auto kern = attn_state8_rows_kernel<D, PAD, E4M3>;
+  auto kern = p.unit_rows == 8 ? attn_state8_rows_kernel<D, 1, PAD, E4M3> : attn_state8_rows_kernel<D, 2, PAD, E4M3>;
   const safedit_status st = set_smem(reinterpret_cast<const void*>(kern), RowsCfg<D>::SMEM);
   if (st != SAFEDIT_OK) return st;
   const dim3 grid{unsigned(p.n_split), unsigned(p.n_tiles), unsigned(BH)};
