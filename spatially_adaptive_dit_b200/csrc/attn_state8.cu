@@ -91,7 +91,6 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   __shared__ uint64_t full[C::NST], empty[C::NST];
   __shared__ int abort_word;
   __shared__ float sm_m[kRowWarps][ROWS], sm_l[kRowWarps][ROWS], sm_range[kRowWarps][2];
-  __shared__ float sm_o[ROWS][D];
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = blockIdx.x, tile = blockIdx.y, bh = blockIdx.z;
@@ -99,6 +98,10 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   const int ns = (p.Nk + kStageKeys - 1) / kStageKeys;  // stages of the whole slice
   const int s_lo = int(int64_t(ns) * split / p.n_split), s_hi = int(int64_t(ns) * (split + 1) / p.n_split);
   const uint32_t ring = (smem_u32(rows_smem) + 1023u) & ~1023u;
+  if (threadIdx.x == kRowWarps * 32) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
@@ -360,28 +363,35 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
       }
     if (lane == 0) sm_range[warp][0] = lv_lo, sm_range[warp][1] = lv_hi;
   }
-  for (int e = threadIdx.x; e < ROWS * D; e += kRowThreads8) (&sm_o[0][0])[e] = 0.f;
   __syncthreads();
-  for (int w = 0; w < kRowWarps; ++w) {  // one warp after another: the sum's order is fixed
-    if (warp == w) {
+  // each warp's scaled output to the ring (its copies have all landed), added
+  // in the warps' order
+  float* const sm_part = reinterpret_cast<float*>(rows_smem);
+  if (warp < kRowWarps) {
 #pragma unroll
-      for (int q = 0; q < NQ; ++q)
+    for (int q = 0; q < NQ; ++q)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 8 * q + 2 * t + e;
-          float mx = -INFINITY;
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * q + 2 * t + e;
+        float mx = -INFINITY;
 #pragma unroll
-          for (int v = 0; v < kRowWarps; ++v) mx = fmaxf(mx, sm_m[v][r]);
-          const float f = m[q][e] == -INFINITY ? 0.f : ex2_approx(m[q][e] - mx);
+        for (int v = 0; v < kRowWarps; ++v) mx = fmaxf(mx, sm_m[v][r]);
+        const float f = m[q][e] == -INFINITY ? 0.f : ex2_approx(m[q][e] - mx);
+        float* row = sm_part + (warp * ROWS + r) * D;
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            sm_o[r][value_col<D>(g, 2 * i)] += o[q][i][e] * f;
-            sm_o[r][value_col<D>(g, 2 * i + 1)] += o[q][i][e + 2] * f;
-          }
+        for (int i = 0; i < NT; ++i) {
+          row[value_col<D>(g, 2 * i)] = o[q][i][e] * f;
+          row[value_col<D>(g, 2 * i + 1)] = o[q][i][e + 2] * f;
         }
-    }
-    __syncthreads();
+      }
   }
+  __syncthreads();
+  auto joined = [&](int e) {  // element e of [ROWS][D]
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) v += sm_part[w * ROWS * D + e];
+    return v;
+  };
   for (int w = 0; w < kRowWarps; ++w) lv_lo = fminf(lv_lo, sm_range[w][0]), lv_hi = fmaxf(lv_hi, sm_range[w][1]);
   float mx = -INFINITY, lx = 0.f;  // of row threadIdx.x
   if (threadIdx.x < ROWS) {
@@ -391,7 +401,7 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   }
   if (p.n_split > 1) {
     const PartView pv = part_view(p, (int64_t(bh) * p.n_tiles + tile) * p.n_split + split, D);
-    for (int e = threadIdx.x; e < p.tile_rows * D; e += kRowThreads8) pv.o[e] = (&sm_o[0][0])[e];
+    for (int e = threadIdx.x; e < p.tile_rows * D; e += kRowThreads8) pv.o[e] = joined(e);
     if (threadIdx.x < p.tile_rows) pv.ml[threadIdx.x * 2] = mx, pv.ml[threadIdx.x * 2 + 1] = lx;
     if (threadIdx.x == 0) pv.range[0] = lv_lo, pv.range[1] = lv_hi;
     return;
@@ -410,46 +420,78 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
     const float inv = ls == 0.f ? 0.f : 1.f / ls;
     const int64_t orow = p.out_scattered ? int64_t(qi) : int64_t(r);
     *reinterpret_cast<uint32_t*>(p.out + b * p.o_sb + h * p.o_sh + orow * p.o_sr + c) =
-        pack_bf16x2(sm_o[rr][c] * inv, sm_o[rr][c + 1] * inv);
+        pack_bf16x2(joined(rr * D + c) * inv, joined(rr * D + c + 1) * inv);
   }
 }
 
 // ------------------------------------------------------------- parts joined
 // One CTA for each query row: m = max m_i, out = sum 2^(m_i - m) O_i /
-// sum 2^(m_i - m) l_i over the row's parts, in their order.
-template <int D>
-__global__ void __launch_bounds__(D) attn_state8_join_kernel(const __grid_constant__ State8Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = threadIdx.x;
+// sum 2^(m_i - m) l_i over the row's parts.  Each warp takes every
+// kJoinWarps-th part and the warps' sums are added in their order, so the
+// result does not depend on timing.  A few microseconds of dependent loads:
+// one thread per column over all parts in turn took 41 us at 200 parts.
+template <int D, int kJoinWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_state8_join_kernel(const __grid_constant__ State8Params p) {
+  __shared__ float sm_red[3][kJoinWarps], sm_l[kJoinWarps], sm_o[kJoinWarps][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pu = blockIdx.x / p.tile_rows, rr = blockIdx.x - pu * p.tile_rows;
   const int unit = p.n_full + pu;
   const int bh = unit / p.n_tiles, r = (unit - bh * p.n_tiles) * p.unit_rows + rr;
-  if (r >= p.n_rows) return;
   const int b = bh / p.H, h = bh - b * p.H;
-  const int qi = p.idx ? __ldg(p.idx + r) : r;
-  if (qi < 0 || qi >= p.Nq) return;  // reported by the attention kernel
+  int qi = -1;
+  if (r < p.n_rows) qi = p.idx ? __ldg(p.idx + r) : r;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (qi < 0 || qi >= p.Nq) return;  // no row, or reported by the attention kernel
   const int64_t rec0 = int64_t(pu) * p.n_split;
-  float m = -INFINITY, lv_lo = INFINITY, lv_hi = -INFINITY;
-  for (int s = 0; s < p.n_split; ++s) {
+  float m = -INFINITY, lo = INFINITY, hi = -INFINITY;
+  for (int s = threadIdx.x; s < p.n_split; s += kJoinWarps * 32) {
     const PartView v = part_view(p, rec0 + s, D);
     m = fmaxf(m, v.ml[rr * 2]);
-    lv_lo = fminf(lv_lo, v.range[0]), lv_hi = fmaxf(lv_hi, v.range[1]);
+    lo = fminf(lo, v.range[0]), hi = fmaxf(hi, v.range[1]);
   }
-  float l = 0.f, acc = 0.f;
+#pragma unroll
+  for (int e = 16; e; e >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, e));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, e));
+  }
+  if (lane == 0) sm_red[0][warp] = m, sm_red[1][warp] = lo, sm_red[2][warp] = hi;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    m = fmaxf(m, sm_red[0][w]);
+    lo = fminf(lo, sm_red[1][w]), hi = fmaxf(hi, sm_red[2][w]);
+  }
+  float l = 0.f, acc[D / 32];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < p.n_split; ++s) {
+  for (int s = warp; s < p.n_split; s += kJoinWarps) {
     const PartView v = part_view(p, rec0 + s, D);
-    const float ms = v.ml[rr * 2];
+    const float ms = v.ml[rr * 2], ls = v.ml[rr * 2 + 1];
+    float x[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) x[e] = v.o[rr * D + lane + 32 * e];
     const float w = ms == -INFINITY ? 0.f : ex2_approx(ms - m);
-    l = fmaf(w, v.ml[rr * 2 + 1], l);
-    if (w != 0.f) acc = fmaf(w, v.o[rr * D + c], acc);
+    l = fmaf(w, ls, l);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, x[e], acc[e]);
   }
-  if (c == 0) {
-    if (lv_hi - lv_lo > kScaleSpread) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) sm_o[warp][lane + 32 * e] = acc[e];
+  if (lane == 0) sm_l[warp] = l;
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float sum = 0.f;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) sum += sm_o[w][threadIdx.x], l += sm_l[w];
+  if (threadIdx.x == 0) {
+    if (hi - lo > kScaleSpread) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
     if (l == 0.f) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
   }
   const int64_t orow = p.out_scattered ? int64_t(qi) : int64_t(r);
-  p.out[b * p.o_sb + h * p.o_sh + orow * p.o_sr + c] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
+  p.out[b * p.o_sb + h * p.o_sh + orow * p.o_sr + threadIdx.x] = __float2bfloat16_rn(l == 0.f ? 0.f : sum / l);
 }
 
 // ------------------------------------------------------------- plan
@@ -482,7 +524,10 @@ static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int
   if (!pl.tc) {
     // one wave of what an SM holds, each part two stages of keys at least
     int64_t split = int64_t(sms) * (D == 64 ? RowsCfg<64>::CTAS : D == 96 ? RowsCfg<96>::CTAS : RowsCfg<128>::CTAS) / units;
-    const int64_t most = (Nk + 2 * kStageKeys - 1) / (2 * kStageKeys);
+    // (beyond 64 parts, which take their time to join, eight)
+    const int64_t stages = (Nk + kStageKeys - 1) / kStageKeys;
+    int64_t most = (stages + 1) / 2;
+    if (most > 64) most = stages / 8 > 64 ? stages / 8 : 64;
     if (split > most) split = most;
     pl.n_split = split > 1 ? int(split) : 1;
     pl.n_parts = split > 1 ? units : 0;
@@ -509,18 +554,18 @@ static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int
   return pl;
 }
 
-template <int D>
+template <int D, int W>
 static safedit_status launch_join(const State8Params& p, int64_t n_parts, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(n_parts * p.tile_rows));
-  cfg.blockDim = dim3(D);
+  cfg.blockDim = dim3(W * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attn_state8_join_kernel<D>, p) != cudaSuccess) return SAFEDIT_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, attn_state8_join_kernel<D, W>, p) != cudaSuccess) return SAFEDIT_ERR_CUDA;
   return after_launch(1);
 }
 
@@ -562,7 +607,8 @@ static safedit_status dispatch_state8(const safedit_tensor* k8, const safedit_te
       st = e4m3 ? launch_rows<D, false, true>(tmK, tmV, p, BH, s) : launch_rows<D, false, false>(tmK, tmV, p, BH, s);
   }
   if (st != SAFEDIT_OK || pl.n_parts == 0) return st;
-  return launch_join<D>(p, pl.n_parts, s);
+  // many parts of few rows, or few parts of many rows
+  return pl.tc ? launch_join<D, 4>(p, pl.n_parts, s) : launch_join<D, 16>(p, pl.n_parts, s);
 }
 
 static safedit_status check_rows16(const safedit_tensor* t) {
