@@ -49,6 +49,7 @@ struct TcCfg {
   static constexpr int SMEM_PLAIN = 1024 + OFF_PAD;
   static constexpr int SMEM_PAD = 1024 + OFF_LIVE + LIVE_WORDS * 4;
   static_assert(SMEM_PAD <= 232448, "shared memory");
+  static_assert(8 * 32 * (2 * D + 16) <= OFF_RAW, "rows on their way out");
   static_assert(256 + 2 * D <= 512, "TMEM columns");
 };
 
@@ -70,6 +71,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
   return v;
+}
+// Asynchronous 16-byte copy, zeros past `bytes` (0 or 16).
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ float lds32(uint32_t at) {
   float v;
@@ -242,34 +247,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           my_q = -1;
         }
       }
-      // ---- this thread's query row: largest magnitude, factor to f16, the
-      // swizzled K-major layout
+      // ---- the warp's 32 query rows: copied piece by piece (16 bytes a lane,
+      // neighbouring lanes on neighbouring pieces) into the swizzled K-major
+      // layout; then each thread takes its own row's largest magnitude and
+      // turns it into f16 in place.  A row to a thread straight from global
+      // memory took 3.5 us, 32 cache lines a load.
       float undo;
       {
-        uint4 v[D / 8];
+        constexpr int UNITS = D / 8;
+        const uint32_t qs = sb + uint32_t(t * C::TILE_BYTES);
+        auto piece = [&](int row, int c) {  // row of the tile, 16-byte piece
+          return qs + uint32_t((c * 8 / C::CH) * C::CHUNK_BYTES) +
+                 tc_swizzle(uint32_t(row * C::ROWB + (c * 8 % C::CH) * 2), C::LAYOUT);
+        };
+        const __nv_bfloat16* const qb = p.q + b * p.q_sb + h * p.q_sh;
+        const int wrow = rr & 96;  // first row of the warp in the tile
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+          const int u = lane + 32 * i, row = u / UNITS, c = u - row * UNITS;
+          const int qi = __shfl_sync(0xffffffffu, my_q, row);
+          cp_async16_zfill(piece(wrow + row, c), qb + (qi < 0 ? 0 : int64_t(qi) * p.q_sr + c * 8), qi < 0 ? 0u : 16u);
+        }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
         uint32_t m = 0u;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.q_sb + h * p.q_sh +
-                                                          int64_t(my_q < 0 ? 0 : my_q) * p.q_sr);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) v[c] = my_q >= 0 ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        for (int c = 0; c < UNITS; ++c) {
+          const uint4 v = lds128(piece(rr & 127, c));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) m = max(m, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
         }
         const float f = query_factor(m, p.scale_log2, undo);
-        const uint32_t qs = sb + uint32_t(t * C::TILE_BYTES);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        for (int c = 0; c < UNITS; ++c) {
+          const uint32_t at = piece(rr & 127, c);
+          const uint4 v = lds128(at);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             o[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
-          const uint32_t off = uint32_t((c * 8 / C::CH) * C::CHUNK_BYTES) +
-                               tc_swizzle(uint32_t((rr & 127) * C::ROWB + (c * 8 % C::CH) * 2), C::LAYOUT);
-          sts128(qs + off, o[0], o[1], o[2], o[3]);
+          sts128(at, o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
         warp_arrive(BAR(Q_FULL + t), lane);
@@ -409,43 +428,68 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool empty = l_run == 0.f;  // O may never have been written
         if (live && whole && empty) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
         const float inv = empty ? 0.f : 1.f / l_run;
-        float* po = nullptr;
-        __nv_bfloat16* orow = nullptr;
+        // Rows leave through shared memory (the query tiles', free by now), so
+        // that a warp's stores run along rows: bf16 rows at once, a part's
+        // fp32 rows half a row at a time.  Rows are 16 bytes apart from a
+        // multiple of 128, which keeps eight lanes on different banks.
+        constexpr int PITCH = 2 * D + 16, UNITS = D / 8;
+        const uint32_t stage = sb + uint32_t(warp * 32 * PITCH);
+        const uint32_t mine = stage + uint32_t(lane * PITCH);
         if (whole) {
-          const int64_t at = p.out_scattered ? int64_t(my_q) : int64_t(my_row);
-          orow = p.out + b * p.o_sb + h * p.o_sh + at * p.o_sr;
-        } else {
-          const PartView pv = part_view(p, rest, D);
-          po = pv.o + int64_t(rr) * D;
-          if (live) {
-            pv.ml[rr * 2] = m_run;
-            pv.ml[rr * 2 + 1] = l_run;
-          }
-        }
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(tO + uint32_t(c), r);
-          tmem_wait_ld();
-          if (!live) continue;
-          if (empty) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = 0u;
-          }
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(orow + c);
+          for (int c = 0; c < D; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(tO + uint32_t(c), r);
+            tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t o[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                o[k] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]) * inv, __uint_as_float(r[8 * e + 2 * k + 1]) * inv);
-              dst[e] = make_uint4(o[0], o[1], o[2], o[3]);
+                o[k] = empty ? 0u
+                             : pack_bf16x2(__uint_as_float(r[8 * e + 2 * k]) * inv,
+                                           __uint_as_float(r[8 * e + 2 * k + 1]) * inv);
+              sts128(mine + uint32_t(c * 2 + e * 16), o[0], o[1], o[2], o[3]);
             }
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(po + c);
+          }
+          __syncwarp();
+          __nv_bfloat16* const ob = p.out + b * p.o_sb + h * p.o_sh;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          for (int i = 0; i < UNITS; ++i) {
+            const int u = lane + 32 * i, row = u / UNITS, c = u - row * UNITS;
+            const int qi = __shfl_sync(0xffffffffu, my_q, row);
+            const int64_t at = p.out_scattered ? int64_t(qi) : int64_t(row0 + (rr & ~31) + row);
+            if (qi >= 0)
+              *reinterpret_cast<uint4*>(ob + at * p.o_sr + c * 8) = lds128(stage + uint32_t(row * PITCH + c * 16));
+          }
+        } else {
+          const PartView pv = part_view(p, rest, D);
+          if (live) {
+            pv.ml[rr * 2] = m_run;
+            pv.ml[rr * 2 + 1] = l_run;
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 16) {
+              uint32_t r[16];
+              tmem_ld16(tO + uint32_t(half * (D / 2) + c), r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                sts128(mine + uint32_t(c * 4 + e * 16), empty ? 0u : r[4 * e], empty ? 0u : r[4 * e + 1],
+                       empty ? 0u : r[4 * e + 2], empty ? 0u : r[4 * e + 3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) {
+              const int u = lane + 32 * i, row = u / UNITS, c = u - row * UNITS;
+              const int qi = __shfl_sync(0xffffffffu, my_q, row);
+              if (qi >= 0)
+                *reinterpret_cast<uint4*>(pv.o + int64_t((rr & ~31) + row) * D + half * (D / 2) + c * 4) =
+                    lds128(stage + uint32_t(row * PITCH + c * 16));
+            }
+            __syncwarp();
           }
         }
       }
