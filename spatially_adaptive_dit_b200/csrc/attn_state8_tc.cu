@@ -42,7 +42,7 @@ struct TcCfg {
   static constexpr int OFF_V = OFF_K + NS * TILE_BYTES;
   static constexpr int OFF_RAW = OFF_V + NS * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_RAW + NR * RAW_BYTES;
-  static constexpr int N_BARS = 2 + 4 * NS + NR + 2 + 2 + 2;
+  static constexpr int N_BARS = 1 + 4 * NS + NR + 2 + 4 + 2;
   static constexpr int OFF_FACT = OFF_BAR + ((N_BARS * 8 + 8 + 15) / 16) * 16;
   static constexpr int OFF_PAD = OFF_FACT + ((NF * 8 * 12 + 15) / 16) * 16;
   static constexpr int OFF_LIVE = OFF_PAD + NF * 128 * 4;
@@ -135,9 +135,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t sb = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   auto BAR = [&](int i) { return sb + uint32_t(C::OFF_BAR) + 8u * uint32_t(i); };
-  constexpr int Q_FULL = 0, K_FULL = 2, K_EMPTY = K_FULL + C::NS, V_FULL = K_EMPTY + C::NS, V_EMPTY = V_FULL + C::NS,
+  constexpr int Q_FULL = 0, K_FULL = 1, K_EMPTY = K_FULL + C::NS, V_FULL = K_EMPTY + C::NS, V_EMPTY = V_FULL + C::NS,
                 RAW_FULL = V_EMPTY + C::NS, S_FULL = RAW_FULL + C::NR,
-                P_FULL = S_FULL + 2, O_FULL = P_FULL + 2, DRAIN = O_FULL + 1;
+                P_FULL = S_FULL + 2, O_FULL = P_FULL + 4, DRAIN = O_FULL + 1;
   static_assert(DRAIN + 1 == C::N_BARS, "barriers");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -199,10 +199,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
 
   if (threadIdx.x == 0) {
+    mbar_init(BAR(Q_FULL), two ? 8 : 4);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(BAR(Q_FULL + t), 4);
       mbar_init(BAR(S_FULL + t), 1);
-      mbar_init(BAR(P_FULL + t), 4);
+      for (int hf = 0; hf < 2; ++hf) mbar_init(BAR(P_FULL + 2 * t + hf), 4);  // halves of the keys
     }
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(BAR(K_FULL + s), kTcWidenThreads / 32);
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           sts128(at, o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
-        warp_arrive(BAR(Q_FULL + t), lane);
+        warp_arrive(BAR(Q_FULL), lane);
       }
 
       const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
@@ -414,10 +414,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             l_run = fmaf(u0 + u1, gg ? inv.y : inv.x, l_run);
           }
           tmem_st16(tS + uint32_t(c * 16), pk);
+          if (c & 1) {  // half of the keys: their products start
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(BAR(P_FULL + 2 * t + c / 2), lane);
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        warp_arrive(BAR(P_FULL + t), lane);
         j = next_live(j + 1);
         slot = slot + 1 == C::NF ? 0 : slot + 1;
       }
@@ -521,12 +523,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_commit(BAR(S_FULL + t));
         }
       };
-      auto issue_pv = [&](int t, int s, bool acc) {
-        const uint64_t vd = vd0 + uint64_t(uint32_t(s * C::TILE_BYTES) >> 4);
+      auto issue_pv = [&](int t, int hf, int s, bool acc) {  // half of the keys
+        const uint64_t vd = vd0 + uint64_t(uint32_t(s * C::TILE_BYTES + hf * 64 * C::ROWB) >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < C::BN / 16; ++kk)
-            mma_ts(tm + 256u + uint32_t(t * D), tm + uint32_t(t * 128 + kk * 8),
+          for (int kk = 0; kk < C::BN / 32; ++kk)
+            mma_ts(tm + 256u + uint32_t(t * D), tm + uint32_t(t * 128 + hf * 32 + kk * 8),
                    vd + (uint32_t(kk * 16 * C::ROWB) >> 4), idesc_pv, (acc || kk > 0) ? 1u : 0u);
         }
       };
@@ -534,8 +536,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (elect_one()) tc_commit(BAR(bar));
       };
       const int n_live = live_count();
-      bool ok = wait_warp(BAR(Q_FULL), 0u, ctl) && (!two || wait_warp(BAR(Q_FULL + 1), 0u, ctl)) &&
-                (n_live == 0 || wait_warp(BAR(K_FULL), 0u, ctl));
+      bool ok = wait_warp(BAR(Q_FULL), 0u, ctl) && (n_live == 0 || wait_warp(BAR(K_FULL), 0u, ctl));
       if (ok && n_live > 0) {
         tc_fence_after();
         issue_qk(0, 0);
@@ -546,19 +547,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int s = j % C::NS, s1 = (j + 1) % C::NS;
         const bool more = j + 1 < n_live;
         if (!(ok = wait_warp(BAR(V_FULL + s), uint32_t((j / C::NS) & 1), ctl))) break;
-        if (!(ok = wait_warp(BAR(P_FULL), uint32_t(j & 1), ctl))) break;
-        tc_fence_after();
-        issue_pv(0, s, j > 0);
+        auto weigh = [&](int t) {  // both halves of tile t's keys, as they come
+          for (int hf = 0; hf < 2; ++hf) {
+            if (!wait_warp(BAR(P_FULL + 2 * t + hf), uint32_t(j & 1), ctl)) return false;
+            tc_fence_after();
+            issue_pv(t, hf, s, j > 0 || hf > 0);
+          }
+          return true;
+        };
+        if (!(ok = weigh(0))) break;
         if (more) {
           if (!(ok = wait_warp(BAR(K_FULL + s1), uint32_t(((j + 1) / C::NS) & 1), ctl))) break;
           tc_fence_after();
           issue_qk(0, s1);
         }
-        if (two) {
-          if (!(ok = wait_warp(BAR(P_FULL + 1), uint32_t(j & 1), ctl))) break;
-          tc_fence_after();
-          issue_pv(1, s, j > 0);
-        }
+        if (two && !(ok = weigh(1))) break;
         commit(V_EMPTY + s);
         if (more) {
           if (two) issue_qk(1, s1);
