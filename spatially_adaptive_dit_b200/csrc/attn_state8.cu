@@ -510,8 +510,12 @@ static int state8_sms() {
   return sms;
 }
 
-// Rows of a slice up to which the warp-level kernel is taken.
-constexpr int64_t kFewRows = 16;
+// Rows of a slice up to which the warp-level kernel is taken.  Measured, us,
+// warp-level / tensor-core kernel: 48 slices x 25600 keys of 96: 16 rows 59 /
+// 123, 32 rows 109 / 124, 48 rows 140 / 126; x 4096 keys: 16 rows 27 / 36, 32
+// rows 40 / 36; 32 slices x 16384 keys of 128: 32 rows 84 / 82; 4 slices: 32
+// rows 25 / 32.
+constexpr int64_t kFewRows = 32;
 
 static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int sms) {
   State8Plan pl;
@@ -533,15 +537,22 @@ static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int
     pl.n_parts = split > 1 ? units : 0;
   } else {
     // The units that do not fill a wave of the SMs run as 2..16 parts over
-    // the key tiles where that ends the call sooner: a CTA costs about
-    // kFixedUs and kTileUs a key tile of 128, the join kJoinUs.
-    constexpr double kFixedUs = 9.0, kTileUs = 1.9, kJoinUs = 5.0;
+    // the key tiles where that ends the call sooner.  Measured on B200: a CTA
+    // costs about kFixedUs and, with both query tiles in use, 1.05 us + 6.8 ns
+    // a column for each key tile of 128; the join kJoinUs and a pass over the
+    // parts' records.  A predicted saving under 3% of the call did not show
+    // (7680 rows x 25600 keys, 48 heads of 96: 3.63 ms whole, 3.72 ms with the
+    // last 108 units in 4 parts; 4096 x 4096: 397 us whole, 369 us with 28
+    // units in 4).
+    constexpr double kFixedUs = 13.0, kJoinUs = 6.0;
     const int64_t nk = (Nk + 127) / 128, tail = units % sms;
-    const double tile_us = kTileUs * (D + 32) / 128.0;
-    double best = kFixedUs + double(nk) * tile_us;
+    const double tile_us = n_rows > 128 ? 1.05 + 0.0068 * D : 1.85;
+    const double whole_us = kFixedUs + double(nk) * tile_us;
+    double best = whole_us - 0.03 * whole_us * double((units + sms - 1) / sms);
     for (int s = 2; tail > 0 && s <= 16 && s <= nk; ++s) {
       const double rounds = double((tail * s + sms - 1) / sms);
-      const double cost = rounds * (kFixedUs + double((nk + s - 1) / s) * tile_us) + kJoinUs;
+      const double record_us = double(tail * s) * pl.tile_rows * D * 8 / 3.0e6;
+      const double cost = rounds * (kFixedUs + double((nk + s - 1) / s) * tile_us) + kJoinUs + record_us;
       if (cost < best) {
         best = cost;
         pl.n_split = s;
