@@ -7,7 +7,7 @@
 // its rounding to 8 bits, so no 16-bit rounding comes between).  Bound by
 // memory: 3 bytes for each 16-bit element.  One CTA holds one block of tokens
 // in registers, reads it once, and walks the heads of its group with the
-// angles of its tokens kept, the next head's loads in flight while this one
+// angles of its tokens kept, the next heads' loads in flight while this one
 // is reduced (one barrier for each head).
 #include <type_traits>
 
@@ -69,6 +69,33 @@ struct StoreCfg {
   static constexpr int MIN_CTAS = (R <= 2 ? 1024 : 512) / MAX_THREADS;
 };
 
+template <typename T>
+constexpr int kStoreDepth = sizeof(T) == 4 ? 3 : 4;  // heads of a block in shared memory
+
+// A slot's two runs of 4 elements -> this thread's place, zeros where there is
+// no row; and back.
+template <typename T, bool HALVES>
+__device__ __forceinline__ void slot_async(uint32_t dst, const T* row, int lo, int hi, bool there) {
+  if constexpr (sizeof(T) == 2 && HALVES) {
+    const uint32_t bytes = there ? 8u : 0u;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(row + lo), "r"(bytes) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + 8u), "l"(row + hi), "r"(bytes) : "memory");
+  } else {
+    const uint32_t bytes = there ? 16u : 0u;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(row + lo), "r"(bytes) : "memory");
+    if constexpr (sizeof(T) == 4)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16u), "l"(row + hi), "r"(bytes) : "memory");
+  }
+}
+template <typename T>
+__device__ __forceinline__ void slot_read(uint32_t (&w)[SlotWords<T>::N], uint32_t at) {
+#pragma unroll
+  for (int e = 0; e < SlotWords<T>::N; e += 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[e]), "=r"(w[e + 1]), "=r"(w[e + 2]), "=r"(w[e + 3])
+                 : "r"(at + uint32_t(e * 4)));
+}
+
 // max(m, |a|, |b|), NaN if one is.
 __device__ __forceinline__ float max_abs3(float m, float a, float b) {
   float r;
@@ -112,27 +139,42 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
     for (int j = 0; j < 4; ++j) c[k][j] = 1.f, s[k][j] = 0.f;
     if (rotate && from[k]) rope_angles(p.tab, p.pos, b, i, slot, 1.f, c[k], s[k]);
   }
-  uint32_t w[C::R][NW];
-  auto load = [&]() {
+  // The next heads' elements are on their way into this thread's own places in
+  // shared memory (so no barrier is needed for them), kStoreDepth<T> heads
+  // deep: registers for one head ahead kept 24 KB in flight on an SM, which
+  // bounds the rate at 4.4 TB/s by the memory's latency alone.
+  constexpr int DEPTH = kStoreDepth<T>;
+  extern __shared__ __align__(16) uint8_t store_ring[];
+  const uint32_t ring = smem_u32(store_ring) + threadIdx.x * uint32_t(NW * 4);
+  auto place = [&](int i, int k) { return ring + uint32_t((i * C::R + k) * int(blockDim.x) * NW * 4); };
+  auto load = [&](int i) {
 #pragma unroll
     for (int k = 0; k < C::R; ++k) {
-#pragma unroll
-      for (int e = 0; e < NW; ++e) w[k][e] = 0u;
-      if (from[k]) {
-        slot_load<T, HALVES>(w[k], from[k], lo, hi);
-        from[k] += p.s_sh[t];
-      }
+      slot_async<T, HALVES>(place(i, k), from[k] ? from[k] : base, lo, hi, from[k] != nullptr);
+      if (from[k]) from[k] += p.s_sh[t];
     }
   };
   const int first = p.row0 + r0 + rr;  // state row of the thread's first row
   uint8_t* to = p.code[t] + b * p.c_sb[t] + h_begin * p.c_sh[t] + int64_t(first) * p.c_sr[t];
   float* to_scale = p.scale[t] + b * p.f_sb[t] + h_begin * p.f_sh[t] + p.row0 / BLOCK + blockIdx.x;
-  load();
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) {
+    if (h_begin + i < h_end) load(i);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  int at = 0;  // (h - h_begin) mod DEPTH
   for (int h = h_begin; h < h_end; ++h) {
     float x[C::R][8];
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
 #pragma unroll
-    for (int k = 0; k < C::R; ++k) slot_widen<T>(w[k], x[k]);
-    if (h + 1 < h_end) load();
+    for (int k = 0; k < C::R; ++k) {
+      uint32_t w[NW];
+      slot_read<T>(w, place(at, k));
+      slot_widen<T>(w, x[k]);
+    }
+    if (h + DEPTH - 1 < h_end) load(at == 0 ? DEPTH - 1 : at - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    at = at + 1 == DEPTH ? 0 : at + 1;
     if (rotate) {
 #pragma unroll
       for (int k = 0; k < C::R; ++k) rope_turn<HALVES>(x[k], c[k], s[k]);
@@ -233,8 +275,13 @@ static safedit_status launch_store(StoreParams& p, int64_t B, int64_t n_heads, i
     p.group_end[t] = int(groups);
   }
   if (groups > 65535) return SAFEDIT_ERR_UNSUPPORTED;
-  state8_store_kernel<T, BLOCK, HALVES>
-      <<<dim3(unsigned(blocks), unsigned(groups), unsigned(B)), threads, 0, s>>>(p);
+  auto kern = state8_store_kernel<T, BLOCK, HALVES>;
+  constexpr int kMost = kStoreDepth<T> * BLOCK * 128 * int(sizeof(T));
+  static_assert(kMost <= 230000, "shared memory");
+  const safedit_status st = set_smem(reinterpret_cast<const void*>(kern), kMost);
+  if (st != SAFEDIT_OK) return st;
+  const int ring_bytes = kStoreDepth<T> * BLOCK * p.slots * 8 * int(sizeof(T));
+  kern<<<dim3(unsigned(blocks), unsigned(groups), unsigned(B)), threads, ring_bytes, s>>>(p);
   return after_launch(1);
 }
 
