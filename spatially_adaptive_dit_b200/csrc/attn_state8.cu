@@ -442,9 +442,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_state8_join_kernel(const
   if (r < p.n_rows) qi = p.idx ? __ldg(p.idx + r) : r;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (qi < 0 || qi >= p.Nq) return;  // no row, or reported by the attention kernel
-  const int64_t rec0 = int64_t(pu) * p.n_split;
+  const int n_rec = p.n_split << p.dual;
+  const int64_t rec0 = int64_t(pu) * n_rec;
   float m = -INFINITY, lo = INFINITY, hi = -INFINITY;
-  for (int s = threadIdx.x; s < p.n_split; s += kJoinWarps * 32) {
+  for (int s = threadIdx.x; s < n_rec; s += kJoinWarps * 32) {
     const PartView v = part_view(p, rec0 + s, D);
     m = fmaxf(m, v.ml[rr * 2]);
     lo = fminf(lo, v.range[0]), hi = fmaxf(hi, v.range[1]);
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_state8_join_kernel(const
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int s = warp; s < p.n_split; s += kJoinWarps) {
+  for (int s = warp; s < n_rec; s += kJoinWarps) {
     const PartView v = part_view(p, rec0 + s, D);
     const float ms = v.ml[rr * 2], ls = v.ml[rr * 2 + 1];
     float x[D / 32];
@@ -496,9 +497,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_state8_join_kernel(const
 
 // ------------------------------------------------------------- plan
 struct State8Plan {
-  bool tc = false;
+  bool tc = false, dual = false;
   int unit_rows = 16, tile_rows = 16, n_tiles = 0, n_full = 0, n_split = 1;
-  int64_t n_parts = 0;  // units that run in parts
+  int64_t n_parts = 0, n_records = 0;  // units that run in parts, and their records
   size_t ws_bytes = 0;
 };
 
@@ -545,23 +546,36 @@ static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int
     // last 108 units in 4 parts; 4096 x 4096: 397 us whole, 369 us with 28
     // units in 4).
     constexpr double kFixedUs = 13.0, kJoinUs = 6.0;
-    const int64_t nk = (Nk + 127) / 128, tail = units % sms;
-    const double tile_us = n_rows > 128 ? 1.05 + 0.0068 * D : 1.85;
-    const double whole_us = kFixedUs + double(nk) * tile_us;
-    double best = whole_us - 0.03 * whole_us * double((units + sms - 1) / sms);
-    for (int s = 2; tail > 0 && s <= 16 && s <= nk; ++s) {
-      const double rounds = double((tail * s + sms - 1) / sms);
-      const double record_us = double(tail * s) * pl.tile_rows * D * 8 / 3.0e6;
-      const double cost = rounds * (kFixedUs + double((nk + s - 1) / s) * tile_us) + kJoinUs + record_us;
-      if (cost < best) {
-        best = cost;
-        pl.n_split = s;
+    const int64_t nk = (Nk + 127) / 128;
+    auto record_us = [&](int64_t records) { return double(records) * pl.tile_rows * D * 8 / 3.0e6; };
+    if (n_rows <= 128) {
+      // Both query tiles on the same rows, every unit in parts.
+      constexpr double kDualTileUs = 1.2;
+      pl.dual = true;
+      double best = 1e30;
+      for (int s = 1; s <= 32 && s <= nk; ++s) {
+        const double rounds = double((units * s + sms - 1) / sms);
+        const double cost = rounds * (kFixedUs + double((nk + s - 1) / s) * kDualTileUs) + record_us(units * s * 2);
+        if (cost < best) best = cost, pl.n_split = s;
       }
+      pl.n_parts = units;
+    } else {
+      const int64_t tail = units % sms;
+      const double tile_us = 1.05 + 0.0068 * D;
+      const double whole_us = kFixedUs + double(nk) * tile_us;
+      double best = whole_us - 0.03 * whole_us * double((units + sms - 1) / sms);
+      for (int s = 2; tail > 0 && s <= 16 && s <= nk; ++s) {
+        const double rounds = double((tail * s + sms - 1) / sms);
+        const double cost =
+            rounds * (kFixedUs + double((nk + s - 1) / s) * tile_us) + kJoinUs + record_us(tail * s);
+        if (cost < best) best = cost, pl.n_split = s;
+      }
+      pl.n_parts = pl.n_split > 1 ? tail : 0;
     }
-    pl.n_parts = pl.n_split > 1 ? tail : 0;
   }
   pl.n_full = int(units - pl.n_parts);
-  if (pl.n_parts) pl.ws_bytes = part_floats(pl.n_parts * pl.n_split, pl.tile_rows, D) * sizeof(float);
+  pl.n_records = (pl.n_parts * pl.n_split) << pl.dual;
+  if (pl.n_parts) pl.ws_bytes = part_floats(pl.n_records, pl.tile_rows, D) * sizeof(float);
   return pl;
 }
 
@@ -706,7 +720,8 @@ extern "C" safedit_status safedit_attn_subset_state8(const safedit_tensor* q, co
   p.unit_rows = pl.unit_rows;
   p.tile_rows = pl.tile_rows;
   p.n_tiles = pl.n_tiles;
-  p.n_records = pl.n_parts * pl.n_split;
+  p.n_records = pl.n_records;
+  p.dual = pl.dual;
   p.part = static_cast<float*>(d_workspace);
   p.status = status_ptr();
   if (!p.status) return SAFEDIT_ERR_CUDA;

@@ -44,7 +44,9 @@ struct State8Params {
   // Schedule: units of query rows (n_tiles of them in a (b, h) slice).  Units
   // below n_full run whole; each later one as n_split parts over the keys,
   // whose records (of `tile_rows` rows, see PartView) are joined afterwards.
-  int n_full, n_split, unit_rows, tile_rows, n_tiles;
+  // With at most 128 rows both query tiles of the tensor-core kernel hold the
+  // same rows and take the key tiles in turn (`dual`, two records a part).
+  int n_full, n_split, unit_rows, tile_rows, n_tiles, dual;
   float* part;
   int64_t n_records;
 };

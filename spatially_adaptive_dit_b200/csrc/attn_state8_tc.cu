@@ -17,6 +17,8 @@
 //     W V_1(j), Q K_1(j+1), so one tile's softmax overlaps the other's MMAs.
 //   * online softmax in base 2 with a lazy rescale (by more than 2^8), scales
 //     of 16 keys at a time folded into the factor and offset of the exponent.
+// With at most 128 query rows both tiles hold the same rows and take the key
+// tiles in turn, each with its own sums, which are joined like parts.
 // Key tiles whose pads are all -inf are skipped by every role.  Every wait is
 // bounded; an expired one raises the CTA's abort flag, drains what is in
 // flight, frees TMEM and returns.
@@ -153,7 +155,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int bh = unit / p.n_tiles;
   const int b = bh / p.H, h = bh - b * p.H;
   const int row0 = (unit - bh * p.n_tiles) * 256;
-  const bool two = row0 + 128 < p.n_rows;  // the second tile has rows
+  const bool dual = p.dual;  // both tiles hold the same rows and take the key tiles in turn
+  const bool two = row0 + 128 < p.n_rows;  // the second tile has rows of its own
   const int nk = (p.Nk + C::BN - 1) / C::BN;
   const int k_lo = whole ? 0 : int(int64_t(nk) * part / p.n_split);
   const int k_hi = whole ? nk : int(int64_t(nk) * (part + 1) / p.n_split);
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
 
   if (threadIdx.x == 0) {
-    mbar_init(BAR(Q_FULL), two ? 8 : 4);
+    mbar_init(BAR(Q_FULL), two || dual ? 8 : 4);
     for (int t = 0; t < 2; ++t) {
       mbar_init(BAR(S_FULL + t), 1);
       for (int hf = 0; hf < 2; ++hf) mbar_init(BAR(P_FULL + 2 * t + hf), 4);  // halves of the keys
@@ -236,9 +239,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ================================================== softmax warpgroups
     setmaxnreg_inc<kTcSoftmaxRegs>();
     const int t = warp >> 2;  // query tile
-    const int rr = threadIdx.x;  // row of the unit
+    const int rr = dual ? threadIdx.x & 127 : threadIdx.x;  // row of the unit
     const int my_row = row0 + rr;
-    if (t == 0 || two) {
+    if (t == 0 || two || dual) {
       int my_q = -1;
       if (my_row < p.n_rows) {
         my_q = p.idx ? __ldg(p.idx + my_row) : my_row;
@@ -299,9 +302,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t tO = tmem + 256u + uint32_t(t * D) + lane_base;
       float m_run = -INFINITY, l_run = 0.f;
       bool ok = true;
-      const int n_live = live_count();
-      int j = next_live(k_lo), slot = 0;
-      for (int it = 0; it < n_live; ++it) {
+      // this tile's key tiles: all of them, or every other one
+      const int step = dual ? 2 : 1, begin = dual ? t : 0;
+      const int n_mine = (live_count() - begin + step - 1) / step;
+      int j = next_live(k_lo), slot = begin;
+      if (begin && n_mine > 0) j = next_live(j + 1);
+      for (int it = 0; it < n_mine; ++it) {
         if (!wait_warp(BAR(S_FULL + t), uint32_t(it & 1), ctl)) {
           ok = false;
           break;
@@ -421,7 +427,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         j = next_live(j + 1);
-        slot = slot + 1 == C::NF ? 0 : slot + 1;
+        if (dual) j = next_live(j + 1);
+        slot += step;
+        if (slot >= C::NF) slot -= C::NF;
       }
       // ---- epilogue: O / l -> bf16 rows, or the part's record
       if (ok && wait_warp(BAR(O_FULL), 0u, ctl)) {
@@ -465,7 +473,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               *reinterpret_cast<uint4*>(ob + at * p.o_sr + c * 8) = lds128(stage + uint32_t(row * PITCH + c * 16));
           }
         } else {
-          const PartView pv = part_view(p, rest, D);
+          const PartView pv = part_view(p, dual ? 2 * rest + t : rest, D);
           if (live) {
             pv.ml[rr * 2] = m_run;
             pv.ml[rr * 2 + 1] = l_run;
@@ -536,37 +544,45 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (elect_one()) tc_commit(BAR(bar));
       };
       const int n_live = live_count();
-      bool ok = wait_warp(BAR(Q_FULL), 0u, ctl) && (n_live == 0 || wait_warp(BAR(K_FULL), 0u, ctl));
-      if (ok && n_live > 0) {
+      // both halves of tile t's weights for its i-th key tile, as they come
+      auto weigh = [&](int t, int s, int i) {
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!wait_warp(BAR(P_FULL + 2 * t + hf), uint32_t(i & 1), ctl)) return false;
+          tc_fence_after();
+          issue_pv(t, hf, s, i > 0 || hf > 0);
+        }
+        return true;
+      };
+      auto keys_there = [&](int j) {
+        if (!wait_warp(BAR(K_FULL + j % C::NS), uint32_t((j / C::NS) & 1), ctl)) return false;
         tc_fence_after();
-        issue_qk(0, 0);
-        if (two) issue_qk(1, 0);
-        commit(K_EMPTY);
+        return true;
+      };
+      bool ok = wait_warp(BAR(Q_FULL), 0u, ctl);
+      for (int j = 0; ok && j < (dual ? 2 : 1) && j < n_live; ++j) {
+        if (!(ok = keys_there(j))) break;
+        issue_qk(dual ? j : 0, j);
+        if (two) issue_qk(1, j);
+        commit(K_EMPTY + j);
       }
       for (int j = 0; ok && j < n_live; ++j) {
-        const int s = j % C::NS, s1 = (j + 1) % C::NS;
-        const bool more = j + 1 < n_live;
+        const int s = j % C::NS;
         if (!(ok = wait_warp(BAR(V_FULL + s), uint32_t((j / C::NS) & 1), ctl))) break;
-        auto weigh = [&](int t) {  // both halves of tile t's keys, as they come
-          for (int hf = 0; hf < 2; ++hf) {
-            if (!wait_warp(BAR(P_FULL + 2 * t + hf), uint32_t(j & 1), ctl)) return false;
-            tc_fence_after();
-            issue_pv(t, hf, s, j > 0 || hf > 0);
-          }
-          return true;
-        };
-        if (!(ok = weigh(0))) break;
+        const int ahead = dual ? 2 : 1, s1 = (j + ahead) % C::NS;
+        const bool more = j + ahead < n_live;
+        const int t = dual ? j & 1 : 0;
+        if (!(ok = weigh(t, s, dual ? j >> 1 : j))) break;
+        if (dual) commit(V_EMPTY + s);
         if (more) {
-          if (!(ok = wait_warp(BAR(K_FULL + s1), uint32_t(((j + 1) / C::NS) & 1), ctl))) break;
-          tc_fence_after();
-          issue_qk(0, s1);
+          if (!(ok = keys_there(j + ahead))) break;
+          issue_qk(t, s1);
         }
-        if (two && !(ok = weigh(1))) break;
-        commit(V_EMPTY + s);
-        if (more) {
-          if (two) issue_qk(1, s1);
-          commit(K_EMPTY + s1);
+        if (!dual) {
+          if (two && !(ok = weigh(1, s, j))) break;
+          commit(V_EMPTY + s);
+          if (more && two) issue_qk(1, s1);
         }
+        if (more) commit(K_EMPTY + s1);
       }
       if (ok) commit(O_FULL);
       // every MMA has completed before TMEM is freed, whoever aborted
@@ -772,9 +788,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (whole) {
           if (lv_hi - lv_lo > kScaleSpread) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
         } else {
-          const PartView pv = part_view(p, rest, D);
-          pv.range[0] = lv_lo;
-          pv.range[1] = lv_hi;
+          for (int e = 0; e < (dual ? 2 : 1); ++e) {
+            const PartView pv = part_view(p, dual ? 2 * rest + e : rest, D);
+            pv.range[0] = lv_lo;
+            pv.range[1] = lv_hi;
+          }
         }
       }
     }

@@ -40,29 +40,24 @@ safedit_status rope_setup(const safedit_rope* rope, const safedit_tensor* pos, i
   constexpr double kInv2Pi = 0.15915494309189533577;
   const int halves = rope->halves;
   int at = 0, pair = 0;
-  auto slot_of = [&](int p, int lo, int hi) {
-    if (p % 4 == 0) {
-      tab->lo[p / 4] = static_cast<uint16_t>(lo);
-      tab->hi[p / 4] = static_cast<uint16_t>(hi);
-    }
+  auto set = [&](int p, double turn, int axis, int lo, int hi) {
+    RopeSlot& sl = tab->slot[p / 4];
+    sl.turn[p % 4] = turn;
+    sl.axes = (p % 4 ? sl.axes : 0u) | uint32_t(axis) << (8 * (p % 4));
+    if (p % 4 == 0) sl.lo = static_cast<uint16_t>(lo), sl.hi = static_cast<uint16_t>(hi);
   };
   for (int a = 0; a < A; ++a) {
     const int s = rope->axis_dim[a];
     const double step = std::pow(rope->theta[a], -2.0 / s);
     double f = 1.0;
     for (int m = 0; m < s / 2; ++m, ++pair, f *= step) {
-      tab->turn[pair] = f * kInv2Pi;
-      tab->axis[pair] = static_cast<uint8_t>(a);
-      slot_of(pair, halves ? at + m : at + 2 * m, halves ? at + m + s / 2 : at + 2 * m + 4);
+      set(pair, f * kInv2Pi, a, halves ? at + m : at + 2 * m, halves ? at + m + s / 2 : at + 2 * m + 4);
     }
     at += s;
   }
   // the rest of the row: pairs that do not turn, 8 consecutive elements a slot
   for (; pair < d / 2; ++pair) {
-    const int e = 2 * pair;
-    tab->turn[pair] = 0.0;
-    tab->axis[pair] = 0;
-    slot_of(pair, e, e + 4);
+    set(pair, 0.0, 0, 2 * pair, 2 * pair + 4);
   }
   view->pos = pos->data;
   view->f32 = pos->dtype == SAFEDIT_F32;
@@ -110,15 +105,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
       return;
     }
   }
-  const int lo = p.tab.lo[slot], hi = p.tab.hi[slot];
+  const RopeSlot& sl = p.tab.slot[slot];
+  const int lo = sl.lo, hi = sl.hi;
   const int64_t rs = p.src_indexed ? i : r, rd = p.dst_indexed ? i : r;
-  float c[4], s[4];
-  rope_angles(p.tab, p.pos, b, i, slot, p.sign, c, s);
   const int h_end = min(p.n_heads, int(blockIdx.y + 1) * p.heads_per_group);
   constexpr int F = kRopeFlight<T>;
-  for (int h0 = blockIdx.y * p.heads_per_group; h0 < h_end; h0 += F) {
-    uint32_t w[F][SlotWords<T>::N];
-    T* to[F];
+  uint32_t w[F][SlotWords<T>::N];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int e = 0; e < F; ++e) {
       const int hh = h0 + e;
@@ -126,19 +119,27 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
       int t = 0;
       while (hh >= p.head_end[t]) ++t;
       const int h = t ? hh - p.head_end[t - 1] : hh;
-      const T* row = static_cast<const T*>(p.src[t]) + b * p.s_sb[t] + h * p.s_sh[t] + rs * p.s_sr[t];
-      to[e] = static_cast<T*>(p.dst[t]) + b * p.d_sb[t] + h * p.d_sh[t] + rd * p.d_sr[t];
-      slot_load<T, HALVES>(w[e], row, lo, hi);
+      slot_load<T, HALVES>(w[e], static_cast<const T*>(p.src[t]) + b * p.s_sb[t] + h * p.s_sh[t] + rs * p.s_sr[t], lo, hi);
     }
+  };
+  load(blockIdx.y * p.heads_per_group);  // on their way while the angles are taken
+  float c[4], s[4];
+  rope_angles(sl, p.pos, b, i, p.sign, c, s);
+  for (int h0 = blockIdx.y * p.heads_per_group; h0 < h_end; h0 += F) {
 #pragma unroll
     for (int e = 0; e < F; ++e) {
-      if (h0 + e >= h_end) break;
+      const int hh = h0 + e;
+      if (hh >= h_end) break;
+      int t = 0;
+      while (hh >= p.head_end[t]) ++t;
+      const int h = t ? hh - p.head_end[t - 1] : hh;
+      T* const to = static_cast<T*>(p.dst[t]) + b * p.d_sb[t] + h * p.d_sh[t] + rd * p.d_sr[t];
       float x[8];
       slot_widen<T>(w[e], x);
       rope_turn<HALVES>(x, c, s);
       if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(to[e] + lo) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4*>(to[e] + hi) = make_float4(x[4], x[5], x[6], x[7]);
+        *reinterpret_cast<float4*>(to + lo) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(to + hi) = make_float4(x[4], x[5], x[6], x[7]);
       } else {
         uint32_t o[4];
 #pragma unroll
@@ -151,13 +152,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
           }
         }
         if constexpr (HALVES) {
-          *reinterpret_cast<uint2*>(to[e] + lo) = make_uint2(o[0], o[1]);
-          *reinterpret_cast<uint2*>(to[e] + hi) = make_uint2(o[2], o[3]);
+          *reinterpret_cast<uint2*>(to + lo) = make_uint2(o[0], o[1]);
+          *reinterpret_cast<uint2*>(to + hi) = make_uint2(o[2], o[3]);
         } else {
-          *reinterpret_cast<uint4*>(to[e] + lo) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(to + lo) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
     }
+    if (h0 + F < h_end) load(h0 + F);
   }
 }
 
@@ -235,9 +237,10 @@ extern "C" safedit_status safedit_rope_rows(const safedit_tensor* src, const saf
   if (d_idx && dst_indexed && index_check_enabled() &&
       (st = launch_index_check(d_idx, int32_t(n), p.limit, p.status, s)) != SAFEDIT_OK)
     return st;
-  // as few head groups as still give every SM two blocks: each group pays for
-  // the angles again
-  const int64_t want = (2 * 148 + blocks * B - 1) / (blocks * B);
+  // as few head groups as still give every SM eight blocks: each group pays
+  // for the angles again, and few large blocks leave SMs idle at the end (4915
+  // rows x 64 heads of 128: two blocks 41-43 us, four 41, eight 37, sixteen 40)
+  const int64_t want = (8 * 148 + blocks * B - 1) / (blocks * B);
   int64_t groups = (heads + 3) / 4;
   if (groups > want) groups = want;
   p.heads_per_group = int((heads + groups - 1) / groups);

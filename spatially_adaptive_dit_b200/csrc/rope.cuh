@@ -19,11 +19,15 @@ namespace sd {
 constexpr int kMaxAxes = 4;
 constexpr int kMaxPairs = 128;  // head dim up to 256
 
+// One slot's constants side by side: lanes of a warp read different slots, and
+// constant memory serves one address at a time, so few wide reads it is.
+struct alignas(16) RopeSlot {
+  double turn[4];    // theta^(-2 m / s) / (2 pi): turns per unit of position
+  uint32_t axes;     // the pairs' axes, a byte each
+  uint16_t lo, hi;   // element offsets of the two runs of 4 elements
+};
 struct RopeTable {
-  double turn[kMaxPairs];    // theta^(-2 m / s) / (2 pi): turns per unit of position
-  uint8_t axis[kMaxPairs];
-  // element offsets of a slot's two runs of 4 elements
-  uint16_t lo[kMaxPairs / 4], hi[kMaxPairs / 4];
+  RopeSlot slot[kMaxPairs / 4];
 };
 
 struct RopePos {
@@ -41,13 +45,13 @@ safedit_status rope_setup(const safedit_rope* rope, const safedit_tensor* pos, i
 // angle is reduced to a fraction of a half turn in fp64 (a position of 2^20
 // at frequency 1 leaves 2^-33 of it); what the fp32 argument of sincospif
 // drops comes back as a first-order term, so both keep fp32 accuracy.
-__device__ __forceinline__ void rope_angles(const RopeTable& tab, const RopePos& v, int b, int64_t i, int slot,
-                                            float sign, float (&c)[4], float (&s)[4]) {
+__device__ __forceinline__ void rope_angles(const RopeSlot& sl, const RopePos& v, int b, int64_t i, float sign,
+                                            float (&c)[4], float (&s)[4]) {
+  const uint32_t axes = sl.axes;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int p = slot * 4 + j;
-    const double f = tab.turn[p];
-    const int64_t at = int64_t(b) * v.sb + i * v.st + int64_t(tab.axis[p]) * v.sa;
+    const double f = sl.turn[j];
+    const int64_t at = int64_t(b) * v.sb + i * v.st + int64_t((axes >> (8 * j)) & 255u) * v.sa;
     const double x = v.f32 ? double(__ldg(static_cast<const float*>(v.pos) + at))
                            : double(__ldg(static_cast<const int32_t*>(v.pos) + at));
     double t = x * f;

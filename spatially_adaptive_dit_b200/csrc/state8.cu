@@ -121,23 +121,24 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
   const int h_begin = group * p.heads_per_group, h_end = min(p.heads[t], h_begin + p.heads_per_group);
   const bool rotate = p.rotate[t];
   int lo = slot * 8, hi = slot * 8 + 4;
-  if (HALVES && p.any_rotate) lo = p.tab.lo[slot], hi = p.tab.hi[slot];
+  if (HALVES && p.any_rotate) lo = p.tab.slot[slot].lo, hi = p.tab.slot[slot].hi;
   const T* from[C::R];  // source row of head h, null: none (its codes are zero)
-  float c[C::R][4], s[C::R][4];
+  int token[C::R];
   const T* base = static_cast<const T*>(p.src[t]) + b * p.s_sb[t] + h_begin * p.s_sh[t];
 #pragma unroll
   for (int k = 0; k < C::R; ++k) {
     const int r = r0 + rr + k * C::RP;
     from[k] = nullptr;
-    int64_t i = r;
+    token[k] = -1;
     if (r < p.n_rows) {
-      if (p.idx) i = __ldg(p.idx + r);
-      if (p.idx && (i < 0 || i >= p.limit)) set_status(p.status, SAFEDIT_ERR_INDEX);
-      else from[k] = base + (p.src_indexed ? i : int64_t(r)) * p.s_sr[t];
+      const int i = p.idx ? __ldg(p.idx + r) : r;
+      if (p.idx && (i < 0 || i >= p.limit)) {
+        set_status(p.status, SAFEDIT_ERR_INDEX);
+      } else {
+        from[k] = base + int64_t(p.src_indexed ? i : r) * p.s_sr[t];
+        token[k] = i;
+      }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c[k][j] = 1.f, s[k][j] = 0.f;
-    if (rotate && from[k]) rope_angles(p.tab, p.pos, b, i, slot, 1.f, c[k], s[k]);
   }
   // The next heads' elements are on their way into this thread's own places in
   // shared memory (so no barrier is needed for them), kStoreDepth<T> heads
@@ -161,6 +162,13 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
   for (int i = 0; i < DEPTH - 1; ++i) {
     if (h_begin + i < h_end) load(i);
     asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  float c[C::R][4], s[C::R][4];
+#pragma unroll
+  for (int k = 0; k < C::R; ++k) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[k][j] = 1.f, s[k][j] = 0.f;
+    if (rotate && token[k] >= 0) rope_angles(p.tab.slot[slot], p.pos, b, token[k], 1.f, c[k], s[k]);
   }
   int at = 0;  // (h - h_begin) mod DEPTH
   for (int h = h_begin; h < h_end; ++h) {
