@@ -48,8 +48,9 @@ struct TcCfg {
   static constexpr int OFF_FACT = OFF_BAR + ((N_BARS * 8 + 8 + 15) / 16) * 16;
   static constexpr int OFF_PAD = OFF_FACT + ((NF * 8 * 12 + 15) / 16) * 16;
   static constexpr int OFF_LIVE = OFF_PAD + NF * 128 * 4;
+  static constexpr int OFF_TOP = OFF_LIVE + LIVE_WORDS * 4;  // the largest pad
   static constexpr int SMEM_PLAIN = 1024 + OFF_PAD;
-  static constexpr int SMEM_PAD = 1024 + OFF_LIVE + LIVE_WORDS * 4;
+  static constexpr int SMEM_PAD = 1024 + OFF_TOP + 4;
   static_assert(SMEM_PAD <= 232448, "shared memory");
   static_assert(8 * 32 * (2 * D + 16) <= OFF_RAW, "rows on their way out");
   static_assert(256 + 2 * D <= 512, "TMEM columns");
@@ -61,6 +62,12 @@ constexpr int kTcWidenThreads = 96;
 constexpr uint32_t kTcSoftmaxRegs = 208, kTcOtherRegs = 88;
 static_assert(256 * kTcSoftmaxRegs + 128 * kTcOtherRegs <= 384 * 168, "register split");
 constexpr uint64_t kTcDrainNs = 1000000000ull;
+// A batch whose largest pad is within this (in log2 units) has log2 vs added to
+// its pads: a sum that matters is off by 2^-13 at most, within the weights' f16
+// rounding (keys 2^13 below the largest have no weight either way).  Beyond
+// it, where the pad absorbs log2 vs and the score itself, as it does in the
+// plain sum, the largest pad comes off first.
+constexpr float kFarPad = 4096.f;
 
 __device__ __forceinline__ uint32_t tc_swizzle(uint32_t off, uint32_t layout) {
   return layout == 2u ? (off ^ (((off >> 7) & 7u) << 4)) : (off ^ (((off >> 7) & 3u) << 4));
@@ -161,22 +168,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int k_lo = whole ? 0 : int(int64_t(nk) * part / p.n_split);
   const int k_hi = whole ? nk : int(int64_t(nk) * (part + 1) / p.n_split);
 
-  // live key tiles: one whose pads are all -inf carries no weight
+  // live key tiles: one whose pads are all -inf carries no weight; and the
+  // batch's largest pad (over all keys, so that every part refers to the same)
   const uint32_t live_s = sb + uint32_t(C::OFF_LIVE);
   const bool skip_tiles = PAD && nk <= C::LIVE_WORDS * 32;
+  float far_pad = 0.f;  // what comes off the exponents first (0 unless it is far)
   if constexpr (PAD) {
     uint32_t* live_bits = reinterpret_cast<uint32_t*>(smem + C::OFF_LIVE);
+    int* const top_bits = reinterpret_cast<int*>(smem + C::OFF_TOP);
+    // fp32 as an integer of the same order
+    auto ordered = [](float v) { const int i = __float_as_int(v); return i >= 0 ? i : i ^ 0x7FFFFFFF; };
     if (threadIdx.x < C::LIVE_WORDS) live_bits[threadIdx.x] = 0u;
+    if (threadIdx.x == 0) *top_bits = ordered(-INFINITY);
     __syncthreads();
-    if (skip_tiles) {
-      const float* pr = p.pad + b * p.pad_sb;
-      for (int j = k_lo + warp; j < k_hi; j += kTcThreads / 32) {
-        bool live = false;
-        for (int c = lane; c < C::BN && j * C::BN + c < p.Nk; c += 32)
-          live |= !(__ldg(pr + j * C::BN + c) == -INFINITY);
-        if (__any_sync(0xffffffffu, live) && lane == 0) atomicOr(live_bits + (j >> 5), 1u << (j & 31));
+    const float* pr = p.pad + b * p.pad_sb;
+    float top = -INFINITY;
+    // four tiles at a time in flight, four pads a lane
+    for (int j0 = warp; j0 < nk; j0 += 4 * (kTcThreads / 32)) {
+      float most[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + e * (kTcThreads / 32), k = j * C::BN + 4 * lane;
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (j < nk && k + 4 <= p.Nk) {
+          v = __ldg(reinterpret_cast<const float4*>(pr + k));
+        } else if (j < nk) {
+          if (k < p.Nk) v.x = __ldg(pr + k);
+          if (k + 1 < p.Nk) v.y = __ldg(pr + k + 1);
+          if (k + 2 < p.Nk) v.z = __ldg(pr + k + 2);
+        }
+        most[e] = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+        if (v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w) most[e] = INFINITY;  // a NaN is no mask
+        top = fmaxf(top, most[e]);
+      }
+      if (skip_tiles) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + e * (kTcThreads / 32);
+          if (__any_sync(0xffffffffu, most[e] != -INFINITY) && lane == 0 && j >= k_lo && j < k_hi)
+            atomicOr(live_bits + (j >> 5), 1u << (j & 31));
+        }
       }
     }
+    atomicMax(top_bits, ordered(top));
+    __syncthreads();
+    const int t = *top_bits;
+    top = pad_log2(__int_as_float(t >= 0 ? t : t ^ 0x7FFFFFFF));
+    if (fabsf(top) > kFarPad && fabsf(top) < INFINITY) far_pad = top;
   }
   auto live_word = [&](int w) -> uint32_t { return __float_as_uint(lds32(live_s + uint32_t(w) * 4u)); };
   // first live tile at or after j (k_hi if none)
@@ -338,20 +376,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           lv[g + 2] = __uint_as_float(l4.z), lv[g + 3] = __uint_as_float(l4.w);
         }
         tmem_wait_ld();
-        if (PAD || ragged) {  // exponents undo ks x + pad; kf has done its part
+        if constexpr (PAD) {  // exponents undo ks x + pad + log2 vs; kf and lv have done their part
+          // (the pads of 16 keys are read together: one read at a time, each
+          // waited for, cost a third of the tile)
 #pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            if constexpr (PAD) {
-              const uint4 pd = lds128(pads + uint32_t(c * 4));
-              x[c] = fmaf(x[c], kf[c / 16], __uint_as_float(pd.x));
-              x[c + 1] = fmaf(x[c + 1], kf[c / 16], __uint_as_float(pd.y));
-              x[c + 2] = fmaf(x[c + 2], kf[c / 16], __uint_as_float(pd.z));
-              x[c + 3] = fmaf(x[c + 3], kf[c / 16], __uint_as_float(pd.w));
-            } else {
+          for (int g = 0; g < 8; ++g) {
+            uint4 pd[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[c + e] = c + e < lim ? x[c + e] * kf[c / 16] : -INFINITY;
+            for (int e = 0; e < 4; ++e) pd[e] = lds128(pads + uint32_t(g * 64 + e * 16));
+            const uint64_t kf2 = f2_pack(kf[g], kf[g]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float* y = x + 16 * g + 4 * e;
+              f2_unpack(f2_fma(f2_pack(y[0], y[1]), kf2, f2_pack(__uint_as_float(pd[e].x), __uint_as_float(pd[e].y))),
+                        y[0], y[1]);
+              f2_unpack(f2_fma(f2_pack(y[2], y[3]), kf2, f2_pack(__uint_as_float(pd[e].z), __uint_as_float(pd[e].w))),
+                        y[2], y[3]);
             }
           }
+          if (far_pad != 0.f) {  // the pads here lack log2 vs
+            const uint64_t off = f2_pack(-far_pad, -far_pad);
+#pragma unroll
+            for (int c = 0; c < 128; c += 2) {
+              const float v = lv[c / 16];
+              f2_unpack(f2_add(f2_add(f2_pack(x[c], x[c + 1]), off), f2_pack(v, v)), x[c], x[c + 1]);
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < 8; ++g) kf[g] = 1.f, lv[g] = 0.f;
+        } else if (ragged) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) x[c] = c < lim ? x[c] * kf[c / 16] : -INFINITY;
 #pragma unroll
           for (int g = 0; g < 8; ++g) kf[g] = 1.f;
         }
@@ -389,7 +444,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-        const uint64_t negm2 = f2_pack(neg_m, neg_m);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float2 inv = lds64(fact + uint32_t(64 + c * 8));
@@ -398,16 +452,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int gg = 0; gg < 2; ++gg) {
             const int g = 2 * c + gg;
             const float off = lv[g] + neg_m;
-            const uint64_t kf2 = f2_pack(kf[g], kf[g]), off2 = f2_pack(off, off), lv2 = f2_pack(lv[g], lv[g]);
+            const uint64_t kf2 = f2_pack(kf[g], kf[g]), off2 = f2_pack(off, off);
             uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const uint64_t xx = f2_pack(x[16 * g + 2 * e], x[16 * g + 2 * e + 1]);
-              // with pads the difference to the reference comes first: a pad
-              // of the type's lowest value absorbs everything added to it
-              const uint64_t a2 = PAD ? f2_add(f2_add(xx, negm2), lv2) : f2_fma(xx, kf2, off2);
               float a0, a1;
-              f2_unpack(a2, a0, a1);
+              f2_unpack(PAD ? f2_add(xx, off2) : f2_fma(xx, kf2, off2), a0, a1);
               const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
               if (e & 1)
                 s1 = f2_add(s1, f2_pack(p0, p1));
@@ -694,7 +745,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // products took the weights of tile `it - NS` from both query tiles, so
     // nobody reads that slot any more, and tile `it + 1` takes it.  Their loads
     // go out a step before.
-    float next_ks = 0.f, next_vs = 1.f, next_pad[2] = {0.f, 0.f};
+    float next_ks = 0.f, next_vs = 1.f, next_pad[2] = {0.f, 0.f}, next_pvs[2] = {1.f, 1.f};
     auto fetch = [&](int kt) {
       const int key = kt * C::BN + tid * 16;
       if (tid < 8 && key < p.Nk) {
@@ -706,6 +757,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int e = 0; e < 2; ++e) {
           const int c = tid + e * kTcWidenThreads, k = kt * C::BN + c;
           if (c < C::BN) next_pad[e] = k < p.Nk ? __ldg(padb + k) : -INFINITY;
+          if (c < C::BN && k < p.Nk) next_pvs[e] = __ldg(vsb + (k >> p.block_log2));
         }
       }
     };
@@ -738,7 +790,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int c = tid + e * kTcWidenThreads;
-          if (c < C::BN) sts32(sb + uint32_t(C::OFF_PAD + slot * 512 + c * 4), pad_log2(next_pad[e]));
+          if (c < C::BN) {
+            const float v = pad_log2(next_pad[e]);
+            sts32(sb + uint32_t(C::OFF_PAD + slot * 512 + c * 4),
+                  far_pad != 0.f || v == -INFINITY ? v : v + __log2f(next_pvs[e]));
+          }
         }
       }
     };
