@@ -49,8 +49,9 @@ struct TcCfg {
   static constexpr int OFF_PAD = OFF_FACT + ((NF * 8 * 12 + 15) / 16) * 16;
   static constexpr int OFF_LIVE = OFF_PAD + NF * 128 * 4;
   static constexpr int OFF_TOP = OFF_LIVE + LIVE_WORDS * 4;  // the largest pad
+  static constexpr int OFF_DEAD = OFF_TOP + 4;               // a byte for each 32 pads of a slot: one is -inf
   static constexpr int SMEM_PLAIN = 1024 + OFF_PAD;
-  static constexpr int SMEM_PAD = 1024 + OFF_TOP + 4;
+  static constexpr int SMEM_PAD = 1024 + OFF_DEAD + NF * 4;
   static_assert(SMEM_PAD <= 232448, "shared memory");
   static_assert(8 * 32 * (2 * D + 16) <= OFF_RAW, "rows on their way out");
   static_assert(256 + 2 * D <= 512, "TMEM columns");
@@ -165,13 +166,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const bool dual = p.dual;  // both tiles hold the same rows and take the key tiles in turn
   const bool two = row0 + 128 < p.n_rows;  // the second tile has rows of its own
   const int nk = (p.Nk + C::BN - 1) / C::BN;
-  const int k_lo = whole ? 0 : int(int64_t(nk) * part / p.n_split);
-  const int k_hi = whole ? nk : int(int64_t(nk) * (part + 1) / p.n_split);
+  int k_lo = whole ? 0 : int(int64_t(nk) * part / p.n_split);
+  int k_hi = whole ? nk : int(int64_t(nk) * (part + 1) / p.n_split);
 
   // live key tiles: one whose pads are all -inf carries no weight; and the
   // batch's largest pad (over all keys, so that every part refers to the same)
   const uint32_t live_s = sb + uint32_t(C::OFF_LIVE);
-  const bool skip_tiles = PAD && nk <= C::LIVE_WORDS * 32;
+  bool skip_tiles = PAD && nk <= C::LIVE_WORDS * 32;
   float far_pad = 0.f;  // what comes off the exponents first (0 unless it is far)
   if constexpr (PAD) {
     uint32_t* live_bits = reinterpret_cast<uint32_t*>(smem + C::OFF_LIVE);
@@ -238,6 +239,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     return n;
   };
+
+  if constexpr (PAD) {  // live tiles that lie together (padding at an end): a shorter range, nothing to skip
+    if (skip_tiles) {
+      const int n = live_count(), first = next_live(k_lo);
+      int j = first;
+      while (j < k_hi && next_live(j) == j) ++j;
+      if (n == 0 || j - first == n) {
+        k_lo = n ? first : k_lo;
+        k_hi = k_lo + n;
+        skip_tiles = false;
+      }
+    }
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(BAR(Q_FULL), two || dual ? 8 : 4);
@@ -669,10 +683,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sts128(a0, o[0], o[1], o[2], o[3]);
       sts128(a1, o[4], o[5], o[6], o[7]);
     };
-    // masked keys: zeros, whatever the codes (NaN) are
-    auto clear_dead = [&](uint4& v, uint32_t pads, int r) {
-      if constexpr (PAD) {
-        if (lds32(pads + uint32_t(r * 4)) == -INFINITY) v = make_uint4(0u, 0u, 0u, 0u);
+    // Rows of masked keys back to zero, whatever their codes (NaN) became.
+    // (int8 has no NaN: what it holds, a weight of 0 takes out.)
+    auto clear_dead = [&](uint32_t to, uint32_t pads) {
+#pragma unroll 1
+      for (int r = tid; r < C::BN; r += kTcWidenThreads) {
+        if (lds32(pads + uint32_t(r * 4)) != -INFINITY) continue;
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c)
+          sts128(to + uint32_t((c * 8 / C::CH) * C::CHUNK_BYTES) +
+                     tc_swizzle(uint32_t(r * C::ROWB + (c * 8 % C::CH) * 2), C::LAYOUT),
+                 0u, 0u, 0u, 0u);
       }
     };
     constexpr int RPP = kTcWidenThreads / UPR;  // d = 64, 128: rows a pass
@@ -683,7 +704,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t p0 = chunk0 + tc_swizzle(in_row + (swap ? 16u : 0u), C::LAYOUT);
     const uint32_t p1 = chunk0 + tc_swizzle(in_row + (swap ? 0u : 16u), C::LAYOUT);
     // the loads of four units go out before the first is widened
-    auto widen = [&](uint32_t raw, uint32_t to, uint32_t pads) {
+    auto widen = [&](uint32_t raw, uint32_t to) {
       if constexpr (D == 96) {
 #pragma unroll
         for (int i0 = 0; i0 < 8; i0 += 4) {
@@ -692,7 +713,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int i = 0; i < 4; ++i) {
             const int r = i0 + i < 6 ? tid : 96 + lane, c = i0 + i < 6 ? i0 + i : (tid >> 5) * 2 + i0 + i - 6;
             v[i] = lds128(raw + uint32_t(r * D + c * 16));
-            clear_dead(v[i], pads, r);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -710,7 +730,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int i = i0; i < i0 + 4 && i < PASSES; ++i) {
             if (i + 1 < PASSES || u_row + i * RPP < 128) {
               v[i - i0] = lds128(raw + uint32_t(tid * 16 + i * RPP * D));
-              clear_dead(v[i - i0], pads, u_row + i * RPP);
             }
           }
 #pragma unroll
@@ -794,6 +813,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const float v = pad_log2(next_pad[e]);
             sts32(sb + uint32_t(C::OFF_PAD + slot * 512 + c * 4),
                   far_pad != 0.f || v == -INFINITY ? v : v + __log2f(next_pvs[e]));
+            if constexpr (E4M3) {  // a whole warp: 32 keys
+              const bool any = __any_sync(0xffffffffu, v == -INFINITY);
+              if (lane == 0)
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(sb + uint32_t(C::OFF_DEAD + slot * 4 + c / 32)),
+                             "r"(uint32_t(any))
+                             : "memory");
+            }
           }
         }
       }
@@ -811,15 +837,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int kt1 = next_live(kt + 1), slot1 = slot + 1 == C::NF ? 0 : slot + 1;
       const bool more = it + 1 < n_live;
       if (more) fetch(kt1);
+      bool dead = false;  // a key of this tile is masked
+      if constexpr (PAD && E4M3) dead = __float_as_uint(lds32(sb + uint32_t(C::OFF_DEAD + slot * 4))) != 0u;
       for (int kv = 0; ok && kv < 2; ++kv) {
         const int n = 2 * it + kv, raw = n % C::NR;
         ok = wait_warp(BAR(RAW_FULL + raw), uint32_t((n / C::NR) & 1), ctl) &&
              wait_warp(BAR((kv ? V_EMPTY : K_EMPTY) + s), ph, ctl);
         if (ok) {
           if (kv && more) publish(kt1, slot1);
-          widen(sb + uint32_t(C::OFF_RAW + raw * C::RAW_BYTES),
-                sb + uint32_t((kv ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES),
-                sb + uint32_t(C::OFF_PAD + slot * 512));
+          const uint32_t to = sb + uint32_t((kv ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES);
+          widen(sb + uint32_t(C::OFF_RAW + raw * C::RAW_BYTES), to);
+          if constexpr (PAD && E4M3) {
+            if (dead) {  // all three warps see the same; every row has been written
+              bar_any(2, kTcWidenThreads, false);
+              clear_dead(to, sb + uint32_t(C::OFF_PAD + slot * 512));
+            }
+          }
           fence_proxy_async_smem();
           warp_arrive(BAR((kv ? V_FULL : K_FULL) + s), lane);
         }
