@@ -527,12 +527,11 @@ static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int
   const int64_t units = pl.n_tiles * BH;
   if (units == 0) return pl;
   if (!pl.tc) {
-    // one wave of what an SM holds, each part two stages of keys at least
+    // one wave of what an SM holds, each part kPartStages stages of keys at
+    // least: the join is a launch of its own
+    constexpr int kPartStages = 8;
     int64_t split = int64_t(sms) * (D == 64 ? RowsCfg<64>::CTAS : D == 96 ? RowsCfg<96>::CTAS : RowsCfg<128>::CTAS) / units;
-    // (beyond 64 parts, which take their time to join, eight)
-    const int64_t stages = (Nk + kStageKeys - 1) / kStageKeys;
-    int64_t most = (stages + 1) / 2;
-    if (most > 64) most = stages / 8 > 64 ? stages / 8 : 64;
+    const int64_t most = (Nk + kStageKeys - 1) / kStageKeys / kPartStages;
     if (split > most) split = most;
     pl.n_split = split > 1 ? int(split) : 1;
     pl.n_parts = split > 1 ? units : 0;
@@ -545,20 +544,21 @@ static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int
     // (7680 rows x 25600 keys, 48 heads of 96: 3.63 ms whole, 3.72 ms with the
     // last 108 units in 4 parts; 4096 x 4096: 397 us whole, 369 us with 28
     // units in 4).
-    constexpr double kFixedUs = 13.0, kJoinUs = 6.0;
+    constexpr double kFixedUs = 13.0, kJoinUs = 8.0;
     const int64_t nk = (Nk + 127) / 128;
     auto record_us = [&](int64_t records) { return double(records) * pl.tile_rows * D * 8 / 3.0e6; };
     if (n_rows <= 128) {
-      // Both query tiles on the same rows, every unit in parts.
-      constexpr double kDualTileUs = 1.2;
-      pl.dual = true;
-      double best = 1e30;
+      // Both query tiles on the same rows, every unit in parts; or one tile
+      // and no join, where there are few keys.
+      constexpr double kDualTileUs = 1.2, kOneTileUs = 1.85;
+      double best = double((units + sms - 1) / sms) * (kFixedUs + double(nk) * kOneTileUs);
       for (int s = 1; s <= 32 && s <= nk; ++s) {
         const double rounds = double((units * s + sms - 1) / sms);
-        const double cost = rounds * (kFixedUs + double((nk + s - 1) / s) * kDualTileUs) + record_us(units * s * 2);
-        if (cost < best) best = cost, pl.n_split = s;
+        const double cost =
+            rounds * (kFixedUs + double((nk + s - 1) / s) * kDualTileUs) + kJoinUs + record_us(units * s * 2);
+        if (cost < best) best = cost, pl.n_split = s, pl.dual = true;
       }
-      pl.n_parts = units;
+      pl.n_parts = pl.dual ? units : 0;
     } else {
       const int64_t tail = units % sms;
       const double tile_us = 1.05 + 0.0068 * D;

@@ -848,16 +848,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int n = 2 * it + kv, raw = n % C::NR;
         ok = wait_warp(BAR(RAW_FULL + raw), uint32_t((n / C::NR) & 1), ctl) &&
              wait_warp(BAR((kv ? V_EMPTY : K_EMPTY) + s), ph, ctl);
+        const uint32_t to = sb + uint32_t((kv ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES);
         if (ok) {
           if (kv && more) publish(kt1, slot1);
-          const uint32_t to = sb + uint32_t((kv ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES);
           widen(sb + uint32_t(C::OFF_RAW + raw * C::RAW_BYTES), to);
-          if constexpr (PAD && E4M3) {
-            if (dead) {  // all three warps see the same; every row has been written
-              bar_any(2, kTcWidenThreads, false);
-              clear_dead(to, sb + uint32_t(C::OFF_PAD + slot * 512));
-            }
+        }
+        if constexpr (PAD && E4M3) {
+          if (dead) {  // all three warps see the same, and come here whether or not a wait ran out
+            ok = !bar_any(2, kTcWidenThreads, !ok);
+            if (ok) clear_dead(to, sb + uint32_t(C::OFF_PAD + slot * 512));
           }
+        }
+        if (ok) {
           fence_proxy_async_smem();
           warp_arrive(BAR((kv ? V_FULL : K_FULL) + s), lane);
         }

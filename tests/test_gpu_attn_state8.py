@@ -350,3 +350,85 @@ def test_a_step_of_the_trajectory(kind):
     ref = torch.softmax(qq @ kt.transpose(2, 3) * d ** -0.5, -1) @ vv
     got = out[:, :, idx_s.long()].double().cpu()
     assert float((got - ref).norm() / ref.norm()) <= 2.0 ** -4 * 1.5
+
+
+@pytest.mark.parametrize("n", (1, 12, 40, 100, 300))
+@pytest.mark.parametrize("kind", CODES)
+@pytest.mark.parametrize("masked", (False, True))
+def test_waits_that_run_out_end_the_call(n, kind, masked):
+    """With no time to wait every role gives up: reported, the device stays usable, and the next call is right."""
+    B, H, N, d, block = 1, 3, 2000, 96, 64
+    st = state(B, H, N, d, kind, block, 1), state(B, H, N, d, kind, block, 2)
+    q = rows((B, H, n, d), BF, 3)
+    pad = None
+    if masked:
+        pad = padded(B, N)
+        pad[:, 5::7] = -math.inf
+        pad[:, 1500:] = -math.inf
+    first = run(q, st, block, pad=pad)
+    old = sd().safedit_debug_set_wait_limit_ns(0)
+    try:
+        run(q, st, block, pad=pad, status=sd().ERR_TIMEOUT)
+    finally:
+        sd().safedit_debug_set_wait_limit_ns(old)
+    again = run(q, st, block, pad=pad)
+    assert torch.equal(first, again)
+    close(again, *attend(q, st, block, None, pad))
+
+
+@pytest.mark.parametrize("n", (1, 20, 100, 300))
+def test_heads_that_share_a_state(n):
+    """Codes and scales of one head broadcast to all (stride 0), pads of one batch to both."""
+    B, H, N, d, block = 2, 4, 700, 64, 32
+    (kc, ks), (vc, vs) = state(B, 1, N, d, "e4m3", block, 1), state(B, 1, N, d, "e4m3", block, 2)
+    k8, v8 = (c.expand(B, H, N, d) for c in (kc, vc))
+    kf, vf = (f.expand(B, H, f.shape[2]) for f in (ks, vs))
+    pad = padded(1, N)
+    pad[:, 600:] = -math.inf
+    pad = pad.expand(B, N)
+    q = rows((B, H, n, d), BF, 3)
+    close(run(q, ((k8, kf), (v8, vf)), block, pad=pad), *attend(q, ((k8, kf), (v8, vf)), block, None, pad))
+
+
+@pytest.mark.parametrize("n", (1, 40, 260))
+@pytest.mark.parametrize("what", ("hole", "head", "all far", "far apart", "mixed"))
+def test_pads_of_every_size(n, what):
+    """Live tiles apart from one another, masked keys in front, pads far from 0 in both directions and beside each
+    other; scales that differ."""
+    B, H, N, d, block = 2, 2, 1500, 128, 16
+    st = state(B, H, N, d, "e4m3", block, 1), state(B, H, N, d, "e4m3", block, 2, spread=4.0)
+    q = rows((B, H, n, d), BF, 3)
+    pad = padded(B, N)
+    pad.copy_(torch.randn(B, N, generator=torch.Generator().manual_seed(4)))
+    if what == "hole":
+        pad[0, 128:512] = pad[0, 700:1290] = -math.inf
+        pad[1, 3:1400:2] = -math.inf
+    elif what == "head":
+        pad[:, :1111] = -math.inf
+    elif what == "all far":
+        pad += 20000.0 * torch.tensor([[1.0], [-1.0]], device=DEV)
+    elif what == "far apart":
+        pad[:, ::3] -= 10000.0
+        pad[1, 1::3] -= 1e30
+    else:
+        pad[0, :] -= 1e9
+        pad[0, 777] = -math.inf
+        pad[1, 500:] = torch.finfo(torch.float32).min
+    # the sums score + pad in fp32, as the kernel (and a plain fp32 sum) has them: what the pad absorbs is gone
+    qq, k = q.double().cpu(), dense(*st[0], block)
+    t = (qq @ k.transpose(2, 3) * d ** -0.5 * math.log2(math.e)).float()
+    p2 = (pad.cpu().double() * math.log2(math.e)).clamp(-3.0e38, 3.0e38).float()
+    p2 = torch.where(pad.cpu() == -math.inf, pad.cpu(), p2)
+    t = (t + p2[:, None, None, :]).double()
+    p = torch.softmax(t * math.log(2.0), -1)
+    v = dense(*st[1], block)
+    out = run(q, st, block, pad=pad)
+    A = p @ v.abs()
+    vf = st[1][1].double().cpu().repeat_interleave(block, 2)[:, :, :N]
+    M = (p * vf[:, :, None, :]).amax(-1, keepdim=True) * st[1][0].float().double().cpu().abs().sum(2, keepdim=True)
+    # a pad of size P leaves the fp32 sums 2^-24 P of a log2 unit, on both sides (20000: 2^-9; beyond 2^24 the sums are
+    # the pads' own multiples and agree), so the weights 2^-8 there; the rest as above
+    extra = 2.0 ** -8 if what == "all far" else 0.0
+    err = (out.double().cpu() - p @ v).abs()
+    assert bool((err <= 2.0 ** -8 * (p @ v).abs() + (2.0 ** -11 + 2.0 ** -12 + extra) * A + 2.0 ** -25 * M).all()), \
+        float((err / (2.0 ** -8 * (p @ v).abs() + (2.0 ** -11 + 2.0 ** -12 + extra) * A + 2.0 ** -25 * M)).max())
