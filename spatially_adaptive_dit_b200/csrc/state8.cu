@@ -33,7 +33,7 @@ struct StoreParams {
   int64_t f_sb[kMaxStoreTensors], f_sh[kMaxStoreTensors];
   int rotate[kMaxStoreTensors];
   int heads[kMaxStoreTensors], group_end[kMaxStoreTensors];  // head groups of tensors 0..t together
-  int heads_per_group, any_rotate, slots, e4m3;
+  int heads_per_group, groups, any_rotate, slots, e4m3;
   int n_rows, row0, state_rows;
   int64_t limit;
   const int* idx;
@@ -62,11 +62,11 @@ __device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float 
 // R = BLOCK / RP rows of each thread.
 template <int BLOCK>
 struct StoreCfg {
-  static constexpr int RP = BLOCK <= 32 ? 16 : 32;
+  static constexpr int RP = BLOCK <= 64 ? 16 : 32;
   static constexpr int R = BLOCK / RP;
   static constexpr int MAX_THREADS = RP * 16;
-  // 64 registers a thread up to two rows, 128 for four
-  static constexpr int MIN_CTAS = (R <= 2 ? 1024 : 512) / MAX_THREADS;
+  // 64, 80 and 128 registers a thread for one, two and four rows
+  static constexpr int MIN_CTAS = (R == 1 ? 1024 : R == 2 ? 768 : 512) / MAX_THREADS;
 };
 
 template <typename T>
@@ -113,11 +113,14 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
   const int rr = threadIdx.x / p.slots, slot = threadIdx.x - rr * p.slots;
   const int lane = threadIdx.x & 31, warps = int(blockDim.x) >> 5;
   const int b = blockIdx.z;
-  const int r0 = blockIdx.x * BLOCK;
-  // this CTA's tensor and heads
+  // the head groups of a block of tokens follow one another, so rotated and
+  // plain tensors (one bound by arithmetic, one by memory) run side by side
+  const int blk = int(blockIdx.x) / p.groups;
+  int group = int(blockIdx.x) - blk * p.groups;
+  const int r0 = blk * BLOCK;
   int t = 0;
-  while (int(blockIdx.y) >= p.group_end[t]) ++t;
-  const int group = int(blockIdx.y) - (t ? p.group_end[t - 1] : 0);
+  while (group >= p.group_end[t]) ++t;
+  if (t) group -= p.group_end[t - 1];
   const int h_begin = group * p.heads_per_group, h_end = min(p.heads[t], h_begin + p.heads_per_group);
   const bool rotate = p.rotate[t];
   int lo = slot * 8, hi = slot * 8 + 4;
@@ -147,20 +150,26 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
   constexpr int DEPTH = kStoreDepth<T>;
   extern __shared__ __align__(16) uint8_t store_ring[];
   const uint32_t ring = smem_u32(store_ring) + threadIdx.x * uint32_t(NW * 4);
-  auto place = [&](int i, int k) { return ring + uint32_t((i * C::R + k) * int(blockDim.x) * NW * 4); };
-  auto load = [&](int i) {
+  const uint32_t pitch = uint32_t(blockDim.x) * uint32_t(NW * 4);  // between a thread's rows and heads
+  const uint32_t ring_end = ring + uint32_t(DEPTH * C::R) * pitch;
+  // this tensor's strides, out of the parameter arrays once
+  const int64_t s_sh = p.s_sh[t], c_sh = p.c_sh[t], c_rows = C::RP * p.c_sr[t];
+  uint32_t put = ring, get = ring;  // where the next head goes, where this one is
+  auto load = [&]() {
 #pragma unroll
     for (int k = 0; k < C::R; ++k) {
-      slot_async<T, HALVES>(place(i, k), from[k] ? from[k] : base, lo, hi, from[k] != nullptr);
-      if (from[k]) from[k] += p.s_sh[t];
+      slot_async<T, HALVES>(put, from[k] ? from[k] : base, lo, hi, from[k] != nullptr);
+      put += pitch;
+      if (from[k]) from[k] += s_sh;
     }
+    if (put == ring_end) put = ring;
   };
   const int first = p.row0 + r0 + rr;  // state row of the thread's first row
   uint8_t* to = p.code[t] + b * p.c_sb[t] + h_begin * p.c_sh[t] + int64_t(first) * p.c_sr[t];
-  float* to_scale = p.scale[t] + b * p.f_sb[t] + h_begin * p.f_sh[t] + p.row0 / BLOCK + blockIdx.x;
+  float* to_scale = p.scale[t] + b * p.f_sb[t] + h_begin * p.f_sh[t] + p.row0 / BLOCK + blk;
 #pragma unroll
   for (int i = 0; i < DEPTH - 1; ++i) {
-    if (h_begin + i < h_end) load(i);
+    if (h_begin + i < h_end) load();
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   float c[C::R][4], s[C::R][4];
@@ -170,19 +179,19 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
     for (int j = 0; j < 4; ++j) c[k][j] = 1.f, s[k][j] = 0.f;
     if (rotate && token[k] >= 0) rope_angles(p.tab.slot[slot], p.pos, b, token[k], 1.f, c[k], s[k]);
   }
-  int at = 0;  // (h - h_begin) mod DEPTH
   for (int h = h_begin; h < h_end; ++h) {
     float x[C::R][8];
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
 #pragma unroll
     for (int k = 0; k < C::R; ++k) {
       uint32_t w[NW];
-      slot_read<T>(w, place(at, k));
+      slot_read<T>(w, get);
+      get += pitch;
       slot_widen<T>(w, x[k]);
     }
-    if (h + DEPTH - 1 < h_end) load(at == 0 ? DEPTH - 1 : at - 1);
+    if (get == ring_end) get = ring;
+    if (h + DEPTH - 1 < h_end) load();
     asm volatile("cp.async.commit_group;" ::: "memory");
-    at = at + 1 == DEPTH ? 0 : at + 1;
     if (rotate) {
 #pragma unroll
       for (int k = 0; k < C::R; ++k) rope_turn<HALVES>(x[k], c[k], s[k]);
@@ -233,9 +242,10 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
     // x * RN(1 / most).  With 16-bit rows the product x qmax is exact, so a
     // tie between two codes is met as one; x * (qmax / most) missed ties and
     // gave the neighbour.
-    const int ex = (int(__float_as_uint(most) >> 23) & 255) - 127;
-    const float m1 = __uint_as_float((__float_as_uint(most) & 0x007FFFFFu) | 0x3F800000u);
-    const float up = __uint_as_float(uint32_t(127 + 6 - ex) << 23) * (qmax / 64.f);  // qmax 2^-ex, exact
+    const uint32_t bits = __float_as_uint(most);
+    const float m1 = __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
+    // qmax 2^-exponent, exact
+    const float up = __uint_as_float((uint32_t(127 + 6 + 127) << 23) - (bits & 0x7F800000u)) * (qmax / 64.f);
     const float inv = 1.f / m1;
     const uint64_t up2 = f2_pack(up, up), inv2 = f2_pack(inv, inv), neg2 = f2_pack(-m1, -m1);
 #pragma unroll
@@ -256,7 +266,7 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
         o0 = pack_codes<false>(y[0], y[1], y[2], y[3]);
         o1 = pack_codes<false>(y[4], y[5], y[6], y[7]);
       }
-      uint8_t* row = to + int64_t(k * C::RP) * p.c_sr[t];
+      uint8_t* row = to + k * c_rows;
       if constexpr (HALVES) {
         *reinterpret_cast<uint32_t*>(row + lo) = o0;
         *reinterpret_cast<uint32_t*>(row + hi) = o1;
@@ -264,7 +274,7 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
         *reinterpret_cast<uint2*>(row + lo) = make_uint2(o0, o1);
       }
     }
-    to += p.c_sh[t];
+    to += c_sh;
     to_scale += p.f_sh[t];
   }
 }
@@ -273,8 +283,10 @@ template <typename T, int BLOCK, bool HALVES>
 static safedit_status launch_store(StoreParams& p, int64_t B, int64_t n_heads, int n_tensors, cudaStream_t s) {
   const int threads = StoreCfg<BLOCK>::RP * p.slots;
   const int64_t blocks = (int64_t(p.n_rows) + BLOCK - 1) / BLOCK;
-  // as few head groups as still give every SM 2048 threads twice over
-  const int64_t ctas = 148 * 2 * (2048 / threads);
+  // as few head groups as still give every SM 2048 threads: each pays for the
+  // angles again (25600 rows x 48 heads of 96, blocks of 64: 154 us, with twice
+  // the groups 164, four times 193)
+  const int64_t ctas = 148 * (2048 / threads);
   int64_t want = (ctas + blocks * B - 1) / (blocks * B);
   p.heads_per_group = int((n_heads + want - 1) / want);
   int64_t groups = 0;
@@ -282,14 +294,15 @@ static safedit_status launch_store(StoreParams& p, int64_t B, int64_t n_heads, i
     groups += (p.heads[t] + p.heads_per_group - 1) / p.heads_per_group;
     p.group_end[t] = int(groups);
   }
-  if (groups > 65535) return SAFEDIT_ERR_UNSUPPORTED;
+  if (groups * blocks > INT32_MAX) return SAFEDIT_ERR_UNSUPPORTED;
+  p.groups = int(groups);
   auto kern = state8_store_kernel<T, BLOCK, HALVES>;
   constexpr int kMost = kStoreDepth<T> * BLOCK * 128 * int(sizeof(T));
   static_assert(kMost <= 230000, "shared memory");
   const safedit_status st = set_smem(reinterpret_cast<const void*>(kern), kMost);
   if (st != SAFEDIT_OK) return st;
   const int ring_bytes = kStoreDepth<T> * BLOCK * p.slots * 8 * int(sizeof(T));
-  kern<<<dim3(unsigned(blocks), unsigned(groups), unsigned(B)), threads, ring_bytes, s>>>(p);
+  kern<<<dim3(unsigned(blocks * groups), 1, unsigned(B)), threads, ring_bytes, s>>>(p);
   return after_launch(1);
 }
 
