@@ -431,10 +431,12 @@ safedit_status safedit_state8_store(const safedit_tensor *src,
  * and the sums are fp32; the probabilities alone are rounded (to f16).
  *
  * A key with key_pad == -inf carries no weight whatever its codes and scales
- * hold.  The other keys' scales must be finite, k_scale >= 0, v_scale > 0,
+ * hold.  The other keys' codes must not be NaN (safedit_state8_store writes
+ * none), their scales must be finite, k_scale >= 0, v_scale > 0,
  * and those of one (b, h) slice of V within a factor of 2^64 of each other;
  * otherwise SAFEDIT_ERR_INVALID_ARG is set and the rows are unspecified.
  * A row whose every key is masked sets SAFEDIT_ERR_MASKED_ROW and gets zeros.
+ * out must not overlap an input.
  *
  * d_workspace / workspace_bytes as in safedit_attn_subset_ws: at least
  * safedit_attn_subset_state8_workspace_size(...) bytes for this call on the

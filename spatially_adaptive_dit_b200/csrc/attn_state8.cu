@@ -23,6 +23,9 @@ namespace sd {
 //   out^T = V^T W^T: the weights' 8 x 8 blocks are transposed between the
 //     lanes; the lane loads, of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, the
 //     elements of column group g, and interleaves them by bytes.
+// One row over 25600 keys of 48 slices (d = 96, 236 MB): 44 us and a join of 5,
+// 5.0 TB/s of the call, against 107 us with the codes straight from global
+// memory into registers (a group of keys ahead was all that fitted).
 // The copies' 128-byte (d = 128) or 64-byte (d = 64) swizzle keeps those reads
 // off each other's banks; rows of 96 bytes are so by themselves.
 constexpr int kRowWarps = 4;                         // warps that multiply
@@ -527,11 +530,15 @@ static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int
   const int64_t units = pl.n_tiles * BH;
   if (units == 0) return pl;
   if (!pl.tc) {
-    // one wave of what an SM holds, each part kPartStages stages of keys at
-    // least: the join is a launch of its own
-    constexpr int kPartStages = 8;
+    // One wave of what an SM holds.  Below 16 stages of keys the join, a launch
+    // of its own, costs more than it saves; above, parts of three stages at
+    // least, and beyond 64 parts, which take their time to join, of eight
+    // (24 slices x 4999 keys, 13 rows: 9 parts 20.0 us, 24 parts 17.4 us; one
+    // slice of 25600 keys: 200 parts were joined in 13 us).
     int64_t split = int64_t(sms) * (D == 64 ? RowsCfg<64>::CTAS : D == 96 ? RowsCfg<96>::CTAS : RowsCfg<128>::CTAS) / units;
-    const int64_t most = (Nk + kStageKeys - 1) / kStageKeys / kPartStages;
+    const int64_t stages = (Nk + kStageKeys - 1) / kStageKeys;
+    int64_t most = stages < 16 ? 1 : stages / 3;
+    if (most > 64) most = stages / 8 > 64 ? stages / 8 : 64;
     if (split > most) split = most;
     pl.n_split = split > 1 ? int(split) : 1;
     pl.n_parts = split > 1 ? units : 0;

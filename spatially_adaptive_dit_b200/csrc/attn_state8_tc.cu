@@ -8,17 +8,32 @@
 //     out for the tensor core.
 //   * warp 11 issues tcgen05.mma.
 //   * warps 8 to 10 stream the codes of K and V by TMA (128 keys a tile) into a
-//     ring and widens codes to f16 into the swizzled tiles that the tensor
+//     ring and widen them to f16 into the swizzled tiles that the tensor
 //     core reads (the tensor core has no product of a 16-bit and an 8-bit
 //     operand, and 8-bit queries or weights would lose what the state keeps),
-//     and computes each tile's scale factors and pads.
+//     and compute each tile's scale factors and pads.
 //   * S_t = Q_t K_j^T into TMEM (fp32), weights back into TMEM as f16 in place
-//     of S_t, O_t += W_t V_j; issue order per key tile W V_0(j), Q K_0(j+1),
-//     W V_1(j), Q K_1(j+1), so one tile's softmax overlaps the other's MMAs.
+//     of S_t, O_t += W_t V_j, each half of the keys as soon as its weights are
+//     there; issue order per key tile W V_0(j), Q K_0(j+1), W V_1(j),
+//     Q K_1(j+1), so one tile's softmax overlaps the other's MMAs.
 //   * online softmax in base 2 with a lazy rescale (by more than 2^8), scales
 //     of 16 keys at a time folded into the factor and offset of the exponent.
 // With at most 128 query rows both tiles hold the same rows and take the key
 // tiles in turn, each with its own sums, which are joined like parts.
+//
+// Bound, at d = 96, by the chain softmax -> products -> softmax of a tile
+// (3300 cycles for 128 keys: 1000 waiting for scores, 300 reading them, 2000
+// for maximum and weights, of which the special function unit needs 1024, or
+// 2048 where the two tiles meet) against 1536 of tensor time; at d = 128 the
+// tensor time is 2048 and the widening of int8 codes (two instructions a pair
+// and an exclusive or, against one conversion of e4m3) shows too.  One wave of
+// 148 CTAs over 8192 keys, us (TFLOP/s): d = 64 127 (620), d = 96 127 / 133
+// (940 / 890, e4m3 / int8), d = 128 139 / 151 (1140 / 1050); the same shapes
+// over a bf16 state take 125 at d = 96.  Measured and not kept: two
+// warpgroups to a tile (24 warps, 80 registers; 154 against 127), halves of
+// the keys with their own score products (N = 64 products read the query tile
+// twice and run at 48 cycles instead of 32; 169 against 139 at d = 128),
+// 1/8 or 1/4 of the exponentials as a polynomial (126 to 131 against 127).
 // Key tiles whose pads are all -inf are skipped by every role.  Every wait is
 // bounded; an expired one raises the CTA's abort flag, drains what is in
 // flight, frees TMEM and returns.
