@@ -7,9 +7,10 @@
 namespace sd {
 
 // ------------------------------------------------------------- few rows
-// One CTA: 8 or 16 query rows of a (b, h) slice and a range of the keys.  Bound by reading the state once: a producer warp keeps a
-// ring of TMA copies of 64 keys' codes of K and V in flight, and four warps
-// take 16 keys each of a stage.  Codes go from shared memory into the
+// One CTA: 8 or 16 query rows of a (b, h) slice and a range of the keys.
+// Bound by reading the state once: a producer warp keeps a ring of TMA copies
+// of 64 keys' codes of K and V in flight, and four warps take 16 keys each of
+// a stage.  Codes go from shared memory into the
 // registers of the warp-level multiplication as they lie: the order of a
 // row's elements inside the product is free as long as both operands agree,
 // so each lane loads runs of consecutive bytes and hands them out as if they

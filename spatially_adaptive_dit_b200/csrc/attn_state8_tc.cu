@@ -807,14 +807,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (key < p.Nk) {
           ks = next_ks;
           lv = __log2f(next_vs);
-          if (!(ks >= 0.f && ks < INFINITY && next_vs > 0.f && next_vs < INFINITY)) {
-            bool used = true;  // a key of the group that is not masked
-            if constexpr (PAD) {
+          const bool bad = !(ks >= 0.f && ks < INFINITY && next_vs > 0.f && next_vs < INFINITY);
+          bool used = true;  // a key of the group that is not masked
+          if constexpr (PAD) {  // looked up where it makes a difference
+            if (bad || fabsf(lv) > 0.5f * kScaleSpread) {
               used = false;
               for (int e = 0; e < 16 && key + e < p.Nk; ++e) used |= __ldg(padb + key + e) != -INFINITY;
             }
-            if (used) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
-            else ks = 0.f, lv = 0.f;
+          }
+          if (!used) {
+            ks = 0.f, lv = 0.f;
+          } else if (bad) {
+            set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
           } else {
             lv_lo = fminf(lv_lo, lv);
             lv_hi = fmaxf(lv_hi, lv);

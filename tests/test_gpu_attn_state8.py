@@ -433,3 +433,21 @@ def test_pads_of_every_size(n, what):
     err = (out.double().cpu() - p @ v).abs()
     assert bool((err <= 2.0 ** -8 * (p @ v).abs() + (2.0 ** -11 + 2.0 ** -12 + extra) * A + 2.0 ** -25 * M).all()), \
         float((err / (2.0 ** -8 * (p @ v).abs() + (2.0 ** -11 + 2.0 ** -12 + extra) * A + 2.0 ** -25 * M)).max())
+
+
+@pytest.mark.parametrize("n", (1, 40, 300))
+@pytest.mark.parametrize("value", (1e-42, 1e-30, 1e30, 3e38, float("inf"), float("nan"), -1.0, 0.0))
+@pytest.mark.parametrize("kind", CODES)
+def test_scales_of_masked_blocks_count_for_nothing(n, value, kind):
+    """Whatever they are, beside blocks in use in the same tile and in tiles of their own."""
+    B, H, N, d, block = 1, 2, 600, 64, 16
+    st = state(B, H, N, d, kind, block, 1), state(B, H, N, d, kind, block, 2)
+    (k8, ks), (v8, vs) = st
+    q = rows((B, H, n, d), BF, 3)
+    pad = padded(B, N)
+    dead = [0, 3, 4, 17, 24, 25, 26, 27, 28, 29, 30, 31, 37]
+    for i in dead:
+        pad[:, i * block: (i + 1) * block] = -math.inf
+    out, A = attend(q, st, block, None, pad)
+    ks[:, :, dead], vs[:, :, dead] = value, value
+    close(run(q, st, block, pad=pad), out, A)
