@@ -343,7 +343,7 @@ typedef struct {
   int32_t halves;      /* 0: neighbouring pairs, 1: pairs half a segment apart */
   int32_t inverse;     /* 0 or 1                                           */
   int32_t axis_dim[4]; /* even (halves == 0) or a multiple of 8 (halves == 1) */
-  double theta[4];     /* > 0, the base of the axis' frequencies           */
+  double theta[4];     /* >= 1, the base of the axis' frequencies          */
 } safedit_rope;
 
 /* For t < n_tensors, r < n, i = d_idx ? d_idx[r] : r (the token):

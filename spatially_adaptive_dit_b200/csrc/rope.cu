@@ -37,7 +37,7 @@ safedit_status rope_setup(const safedit_rope* rope, const safedit_tensor* pos, i
     const int64_t s = rope->axis_dim[a];
     if (s < 1) return SAFEDIT_ERR_INVALID_ARG;
     if (s % (rope->halves ? 8 : 2) != 0) return SAFEDIT_ERR_UNSUPPORTED;
-    if (!(rope->theta[a] > 0.0) || !std::isfinite(rope->theta[a])) return SAFEDIT_ERR_INVALID_ARG;
+    if (!(rope->theta[a] >= 1.0) || !std::isfinite(rope->theta[a])) return SAFEDIT_ERR_INVALID_ARG;
     sum += s;
   }
   if (sum > d) return SAFEDIT_ERR_SHAPE;
@@ -48,7 +48,7 @@ safedit_status rope_setup(const safedit_rope* rope, const safedit_tensor* pos, i
     RopeSlot& sl = tab->slot[p / 4];
     sl.turn[p % 4] = turn;
     sl.axes = (p % 4 ? sl.axes : 0u) | uint32_t(axis) << (8 * (p % 4));
-    if (p % 4 == 0) sl.lo = static_cast<uint16_t>(lo), sl.hi = static_cast<uint16_t>(hi);
+    sl.runs = (p % 4 ? sl.runs : RopeSlot::pack(lo, hi)) | uint32_t(turn != 0.0) << (16 + p % 4);
   };
   for (int a = 0; a < A; ++a) {
     const int s = rope->axis_dim[a];
@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
     }
   }
   const RopeSlot& sl = p.tab.slot[slot];
-  const int lo = sl.lo, hi = sl.hi;
+  const uint32_t runs = sl.runs, turning = RopeSlot::turning(runs);
+  const int lo = RopeSlot::lo(runs), hi = RopeSlot::hi(runs);
   const int64_t rs = p.src_indexed ? i : r, rd = p.dst_indexed ? i : r;
   const int h_end = min(p.n_heads, int(blockIdx.y + 1) * p.heads_per_group);
   constexpr int F = kRopeFlight<T>;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
       T* const to = static_cast<T*>(p.dst[t]) + b * p.d_sb[t] + h * p.d_sh[t] + rd * p.d_sr[t];
       float x[8];
       slot_widen<T>(w[e], x);
-      rope_turn<HALVES>(x, c, s);
+      rope_turn<HALVES>(x, c, s, turning);
       if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4*>(to + lo) = make_float4(x[0], x[1], x[2], x[3]);
         *reinterpret_cast<float4*>(to + hi) = make_float4(x[4], x[5], x[6], x[7]);

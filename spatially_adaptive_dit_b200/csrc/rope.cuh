@@ -24,7 +24,12 @@ constexpr int kMaxPairs = 128;  // head dim up to 256
 struct alignas(16) RopeSlot {
   double turn[4];    // theta^(-2 m / s) / (2 pi): turns per unit of position
   uint32_t axes;     // the pairs' axes, a byte each
-  uint16_t lo, hi;   // element offsets of the two runs of 4 elements
+  uint32_t runs;     // element offsets of the two runs of 4 elements / 4, a byte
+                     // each, and above them the pairs that turn, a bit each
+  __host__ __device__ static uint32_t pack(int lo, int hi) { return uint32_t(lo / 4) | uint32_t(hi / 4) << 8; }
+  __host__ __device__ static int lo(uint32_t runs) { return int(runs & 255u) * 4; }
+  __host__ __device__ static int hi(uint32_t runs) { return int(runs >> 8 & 255u) * 4; }
+  __host__ __device__ static uint32_t turning(uint32_t runs) { return runs >> 16; }
 };
 struct RopeTable {
   RopeSlot slot[kMaxPairs / 4];
@@ -70,16 +75,29 @@ __device__ __forceinline__ void rope_angles(const RopeSlot& sl, const RopePos& v
 }
 
 // Rotates the 8 elements of a slot in fp32: x[0..4) is the run at lo, x[4..8)
-// the run at hi.
+// the run at hi.  Pairs outside `turning` stay as they are: an infinity in one
+// of their elements times the sine's 0 would make the other a NaN.
 template <bool HALVES>
-__device__ __forceinline__ void rope_turn(float (&x)[8], const float (&c)[4], const float (&s)[4]) {
+__device__ __forceinline__ void rope_turn(float (&x)[8], const float (&c)[4], const float (&s)[4],
+                                          uint32_t turning = 15u) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    if (!(turning >> j & 1u)) continue;
     float& a = HALVES ? x[j] : x[2 * j];
     float& b = HALVES ? x[4 + j] : x[2 * j + 1];
     const float y = fmaf(a, c[j], -b * s[j]);
     b = fmaf(a, s[j], b * c[j]);
     a = y;
+  }
+}
+
+// Pairs that do not turn back to what they were, x0.
+template <bool HALVES>
+__device__ __forceinline__ void rope_keep(float (&x)[8], const float (&x0)[8], uint32_t turning) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int a = HALVES ? j : 2 * j, b = HALVES ? 4 + j : 2 * j + 1;
+    if (!(turning >> j & 1u)) x[a] = x0[a], x[b] = x0[b];
   }
 }
 

@@ -126,7 +126,10 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
   const int h_begin = group * p.heads_per_group, h_end = min(p.heads[t], h_begin + p.heads_per_group);
   const bool rotate = p.rotate[t];
   int lo = slot * 8, hi = slot * 8 + 4;
-  if (HALVES && p.any_rotate) lo = p.tab.slot[slot].lo, hi = p.tab.slot[slot].hi;
+  if (HALVES && p.any_rotate) {
+    const uint32_t runs = p.tab.slot[slot].runs;
+    lo = RopeSlot::lo(runs), hi = RopeSlot::hi(runs);
+  }
   const T* from[C::R];  // source row of head h, null: none (its codes are zero)
   int token[C::R];
   const T* base = static_cast<const T*>(p.src[t]) + b * p.s_sb[t] + h_begin * p.s_sh[t];
@@ -213,7 +216,20 @@ __global__ void __launch_bounds__(StoreCfg<BLOCK>::MAX_THREADS, StoreCfg<BLOCK>:
       return __reduce_max_sync(0xffffffffu, lane < warps ? part[buf][lane] : 0u);
     };
     uint32_t top = over_block(__float_as_uint(m) & 0x7FFFFFFFu);
-    if (top >= 0x7F800000u) {  // infinities saturate, NaN becomes 0; reported
+    if (__builtin_expect(top >= 0x7F800000u, 0)) {  // infinities saturate, NaN becomes 0; reported
+      if (rotate) {
+        // this head's place in the ring is written again by the next head's load
+        uint32_t at = (get == ring ? ring_end : get) - uint32_t(C::R) * pitch;
+        const uint32_t turning = RopeSlot::turning(p.tab.slot[slot].runs);
+#pragma unroll
+        for (int k = 0; k < C::R; ++k, at += pitch) {
+          uint32_t w[NW];
+          float x0[8];
+          slot_read<T>(w, at);
+          slot_widen<T>(w, x0);
+          rope_keep<HALVES>(x[k], x0, turning);
+        }
+      }
       uint32_t f = 0u;
 #pragma unroll
       for (int k = 0; k < C::R; ++k)
@@ -390,7 +406,7 @@ extern "C" safedit_status safedit_state8_store(const safedit_tensor* src, const 
   p.n_rows = int(n);
   p.row0 = int(row0);
   p.state_rows = int(N);
-  p.idx = d_idx;
+  p.idx = src_indexed || p.any_rotate ? d_idx : nullptr;  // nothing else reads it
   p.src_indexed = src_indexed;
   p.status = status_ptr();
   if (!p.status) return SAFEDIT_ERR_CUDA;

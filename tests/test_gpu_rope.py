@@ -235,3 +235,28 @@ def test_offsets_past_32_bits():
     sd().safedit_rope_rows([x], [y], pos, sd().rope_spec((d,), (1e4,)))
     expect_status(0)
     close(y, *reference(x, pos, (d,), (1e4,), False, False))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("halves, axes", [(False, (20, 10)), (True, (24, 16))])
+def test_elements_behind_the_last_axis_are_copies(dtype, halves, axes):
+    """Infinities, NaN, the type's ends and zeros of both signs there stay where they are and reach no neighbour, wherever
+    the rows lie and whatever their position."""
+    d, n, end = 64, 32, sum(axes)
+    f = torch.finfo(dtype)
+    x = rows((1, 2, n, d), dtype, 3)
+    special = torch.tensor([float("inf"), -0.0, float("nan"), 0.0, -float("inf"), f.max, f.tiny], dtype=dtype)
+    take = torch.randint(0, 7, (1, 2, n, d - end), generator=torch.Generator().manual_seed(4))
+    x[..., end:] = special[take].to(DEV)
+    pos = positions((1, n, len(axes)), torch.float32, 5)
+    pos[0, 3, 0] = float("inf")  # no position reaches them either
+    y = torch.empty_like(x)
+    sd().safedit_rope_rows([x], [y], pos, sd().rope_spec(axes, (1e4, 100.0), int(halves)))
+    expect_status(0)
+    got, want = y[..., end:].float().cpu(), x[..., end:].float().cpu()
+    nan = want.isnan()
+    assert torch.equal(got.isnan(), nan)
+    assert torch.equal(got[~nan].view(torch.int32), want[~nan].view(torch.int32))
+    keep = [r for r in range(n) if r != 3]
+    ref, mag = reference(x[:, :, keep, :end], pos[:, keep], axes, (1e4, 100.0), halves, False)
+    close(y[:, :, keep, :end], ref, mag)

@@ -213,3 +213,34 @@ def test_offsets_past_32_bits():
     sd().safedit_state8_store([x], [c], [f], 16)
     expect_status(0)
     check_exact(c.contiguous(), f, x, "int8", 16, 0, oc, of)
+
+
+def test_a_value_that_is_not_finite_stays_alone():
+    """An infinity behind the last axis is reported and saturates; its neighbours' codes are what they are without it."""
+    B, H, n, d, axes = 1, 2, 64, 64, (20, 10)
+    x = rows((B, H, n, d), torch.bfloat16, 8)
+    pos, spec = positions((1, n, 2), torch.int32, 9), sd().rope_spec(axes, (1e4, 1e4))
+    x[0, 0, 5, 40] = 50.0  # the block's largest
+    x[0, 0, 7, 31] = x[0, 1, 9, 60] = 0.0
+    at = torch.zeros(B, H, n, d, dtype=torch.bool)
+    at[0, 0, 7, 31] = at[0, 1, 9, 60] = True
+    out = []
+    for value, status in ((0.0, 0), (float("inf"), sd().ERR_INVALID_ARG)):
+        x[at.to(DEV)] = value
+        c, f = new_state(B, H, n, d, "int8", 64)
+        sd().safedit_state8_store([x], [c], [f], 64, rotate=[True], pos=pos, rope=spec)
+        expect_status(status)
+        out.append((raw(c), f.cpu()))
+    assert torch.equal(out[0][1], out[1][1])
+    assert torch.equal(out[0][0][~at], out[1][0][~at])
+    assert bool((out[1][0][at] == 127).all())
+
+
+def test_an_index_that_nothing_reads():
+    """Compact rows that are not rotated: only the index' length counts."""
+    x = rows((1, 2, 40, 64), torch.float16, 3)
+    c, f = new_state(1, 2, 64, 64, "e4m3", 16)
+    c0, f0 = c.clone(), f.clone()
+    sd().safedit_state8_store([x], [c], [f], 16, idx=torch.full((40,), -5, dtype=torch.int32, device=DEV), n_idx=40)
+    expect_status(0)
+    check_exact(c, f, x, "e4m3", 16, 0, c0, f0)

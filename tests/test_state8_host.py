@@ -69,7 +69,7 @@ def test_rope_refusals(sd):
     assert go(r=sd.rope_spec((34, 32, 32), (1e4,) * 3)) == sd.ERR_SHAPE
     assert go(r=sd.rope_spec((32, 0, 32), (1e4,) * 3)) == sd.ERR_INVALID_ARG
     assert go(r=sd.rope_spec((32, 32), (1e4,) * 2)) == sd.ERR_SHAPE
-    for theta in (0.0, -1.0, float("inf"), float("nan")):
+    for theta in (0.0, -1.0, float("inf"), float("nan"), 1e-300, 0.5):
         assert go(r=sd.rope_spec((32, 32, 32), (1e4, theta, 1e4))) == sd.ERR_INVALID_ARG
     bad = sd.rope_spec((32, 32, 32), (1e4,) * 3)
     bad.halves = 2
