@@ -85,9 +85,9 @@ __device__ __forceinline__ void rope_turn(float (&x)[8], const float (&c)[4], co
     if (!(turning >> j & 1u)) continue;
     float& a = HALVES ? x[j] : x[2 * j];
     float& b = HALVES ? x[4 + j] : x[2 * j + 1];
-    const float y = fmaf(a, c[j], -b * s[j]);
-    b = fmaf(a, s[j], b * c[j]);
-    a = y;
+    const float bs = -b * s[j], as = a * s[j];
+    a = fmaf(a, c[j], bs);
+    b = fmaf(b, c[j], as);
   }
 }
 
