@@ -9,8 +9,8 @@
 // in registers, reads it once, and walks the heads of its group with the
 // angles of its tokens kept, the next heads' loads in flight while this one
 // is reduced (one barrier for each head).  K and V of 25600 tokens x 48 heads
-// of 96 (708 MB): 152 us with K rotated, 128 us without (blocks of 64); d =
-// 128: 178 and 156 us, 5.3 and 6.0 TB/s.
+// of 96 (708 MB): 145 us with K rotated, 128 us without (blocks of 64); d =
+// 128: 170 and 156 us, 5.5 and 6.0 TB/s.
 #include <type_traits>
 
 #include <cuda_fp16.h>
@@ -302,8 +302,8 @@ static safedit_status launch_store(StoreParams& p, int64_t B, int64_t n_heads, i
   const int threads = StoreCfg<BLOCK>::RP * p.slots;
   const int64_t blocks = (int64_t(p.n_rows) + BLOCK - 1) / BLOCK;
   // as few head groups as still give every SM 2048 threads: each pays for the
-  // angles again (25600 rows x 48 heads of 96, blocks of 64: 154 us, with twice
-  // the groups 164, four times 193)
+  // angles again (25600 rows x 48 heads of 96, blocks of 64, measured at 154 us: with
+  // twice the groups 164, four times 193)
   const int64_t ctas = 148 * (2048 / threads);
   int64_t want = (ctas + blocks * B - 1) / (blocks * B);
   p.heads_per_group = int((n_heads + want - 1) / want);
