@@ -24,8 +24,8 @@ namespace sd {
 //   out^T = V^T W^T: the weights' 8 x 8 blocks are transposed between the
 //     lanes; the lane loads, of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, the
 //     elements of column group g, and interleaves them by bytes.
-// One row over 25600 keys of 48 slices (d = 96, 236 MB): 44 us and a join of 5,
-// 5.0 TB/s of the call, against 107 us with the codes straight from global
+// One row over 25600 keys of 48 slices (d = 96, 236 MB): 46.6 us, 5.1 TB/s, in
+// clusters of eight (42 us and a join of 5 in nine parts), against 107 us with the codes straight from global
 // memory into registers (a group of keys ahead was all that fitted).
 // The copies' 128-byte (d = 128) or 64-byte (d = 64) swizzle keeps those reads
 // off each other's banks; rows of 96 bytes are so by themselves.
@@ -38,6 +38,7 @@ struct RowsCfg {
   static constexpr int NST = D == 128 ? 4 : (D == 96 ? 5 : 6);  // stages
   static constexpr int CTAS = D == 64 ? 4 : 3;       // on an SM
   static constexpr int SMEM = 1024 + NST * 2 * TILE;
+  static_assert(NST * 2 * TILE >= (kRowWarps + 1) * 16 * D * 4, "the warps' results fit the ring");
 };
 constexpr uint64_t kRowsDrainNs = 1000000000ull;
 
@@ -82,6 +83,27 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   return r;
 }
 
+// The value at shared-memory address `at` of the cluster's CTA `rank`.
+__device__ __forceinline__ float lds_of(uint32_t at, uint32_t rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(at), "r"(rank)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 lds2_of(uint32_t at, uint32_t rank) {
+  float2 v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(at), "r"(rank)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void rows_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 template <int D, int NQ, bool PAD, bool E4M3>
 __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
     attn_state8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -95,6 +117,7 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   __shared__ uint64_t full[C::NST], empty[C::NST];
   __shared__ int abort_word;
   __shared__ float sm_m[kRowWarps][ROWS], sm_l[kRowWarps][ROWS], sm_range[kRowWarps][2];
+  __shared__ __align__(8) float cl_ml[ROWS][2], cl_range[2];  // of all warps, for the cluster
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = blockIdx.x, tile = blockIdx.y, bh = blockIdx.z;
@@ -352,7 +375,9 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
     }
     if (bad) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
   }
-  if (__syncthreads_or(!ok)) return;  // a wait ran out: reported, nothing is written
+  // A wait ran out: reported, nothing is written.  (A cluster's CTAs still meet:
+  // the others read this one's results, which are then as unspecified as its own.)
+  if (__syncthreads_or(!ok) && !p.cluster) return;
 
   // ---- the warps' results joined in shared memory
   if (warp < kRowWarps) {
@@ -402,6 +427,47 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
     for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, sm_m[w][threadIdx.x]);
     for (int w = 0; w < kRowWarps; ++w)
       if (sm_m[w][threadIdx.x] != -INFINITY) lx = fmaf(ex2_approx(sm_m[w][threadIdx.x] - mx), sm_l[w][threadIdx.x], lx);
+  }
+  if (p.cluster) {
+    // ---- the parts joined by the cluster's CTAs: each takes its share of the
+    // elements and adds the parts in their order
+    float* const own = sm_part + kRowWarps * ROWS * D;
+    for (int e = threadIdx.x; e < p.tile_rows * D; e += kRowThreads8) own[e] = joined(e);
+    if (threadIdx.x < ROWS) cl_ml[threadIdx.x][0] = mx, cl_ml[threadIdx.x][1] = lx;
+    if (threadIdx.x == 0) cl_range[0] = lv_lo, cl_range[1] = lv_hi;
+    rows_cluster_sync();
+    const uint32_t own_s = smem_u32(own), ml_s = smem_u32(cl_ml), range_s = smem_u32(cl_range);
+    if (split == 0 && threadIdx.x == 0) {
+      for (int s = 0; s < p.n_split; ++s) {
+        const float2 range = lds2_of(range_s, s);
+        lv_lo = fminf(lv_lo, range.x), lv_hi = fmaxf(lv_hi, range.y);
+      }
+      if (lv_hi - lv_lo > kScaleSpread) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
+    }
+    for (int e = split * kRowThreads8 + threadIdx.x; e < p.tile_rows * D / 2; e += p.n_split * kRowThreads8) {
+      const int rr = e / (D / 2), c = (e - rr * (D / 2)) * 2, r = tile * ROWS + rr;
+      if (r >= p.n_rows) break;
+      const int qi = p.idx ? __ldg(p.idx + r) : r;
+      if (qi < 0 || qi >= p.Nq) continue;
+      float mm = -INFINITY;
+#pragma unroll 4
+      for (int s = 0; s < p.n_split; ++s) mm = fmaxf(mm, lds_of(ml_s + uint32_t(rr * 8), s));
+      float ls = 0.f, a0 = 0.f, a1 = 0.f;
+#pragma unroll 4
+      for (int s = 0; s < p.n_split; ++s) {
+        const float2 ml = lds2_of(ml_s + uint32_t(rr * 8), s), x = lds2_of(own_s + uint32_t(e * 8), s);
+        const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
+        ls = fmaf(w, ml.y, ls);
+        a0 = fmaf(w, x.x, a0);
+        a1 = fmaf(w, x.y, a1);
+      }
+      if (ls == 0.f && c == 0) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      const int64_t orow = p.out_scattered ? int64_t(qi) : int64_t(r);
+      *reinterpret_cast<uint32_t*>(p.out + b * p.o_sb + h * p.o_sh + orow * p.o_sr + c) = pack_bf16x2(a0 * inv, a1 * inv);
+    }
+    rows_cluster_sync();  // nobody leaves while another still reads it
+    return;
   }
   if (p.n_split > 1) {
     const PartView pv = part_view(p, (int64_t(bh) * p.n_tiles + tile) * p.n_split + split, D);
@@ -501,7 +567,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_state8_join_kernel(const
 
 // ------------------------------------------------------------- plan
 struct State8Plan {
-  bool tc = false, dual = false;
+  bool tc = false, dual = false, cluster = false;
   int unit_rows = 16, tile_rows = 16, n_tiles = 0, n_full = 0, n_split = 1;
   int64_t n_parts = 0, n_records = 0;  // units that run in parts, and their records
   size_t ws_bytes = 0;
@@ -531,18 +597,35 @@ static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int
   const int64_t units = pl.n_tiles * BH;
   if (units == 0) return pl;
   if (!pl.tc) {
-    // One wave of what an SM holds.  Below 16 stages of keys the join, a launch
-    // of its own, costs more than it saves; above, parts of three stages at
-    // least, and beyond 64 parts, which take their time to join, of eight
-    // (24 slices x 4999 keys, 13 rows: 9 parts 20.0 us, 24 parts 17.4 us; one
-    // slice of 25600 keys: 200 parts were joined in 13 us).
-    int64_t split = int64_t(sms) * (D == 64 ? RowsCfg<64>::CTAS : D == 96 ? RowsCfg<96>::CTAS : RowsCfg<128>::CTAS) / units;
+    // One wave of what an SM holds.  Parts of three stages at least, joined by
+    // a launch of their own (24 slices x 4999 keys, 13 rows: 9 parts 20.0 us, 24
+    // parts 17.4 us), beyond 64 parts, which take their time to join, of eight
+    // (one slice of 25600 keys: 200 parts were joined in 13 us).
+    const int64_t wave = int64_t(sms) * (D == 64 ? RowsCfg<64>::CTAS : D == 96 ? RowsCfg<96>::CTAS : RowsCfg<128>::CTAS);
     const int64_t stages = (Nk + kStageKeys - 1) / kStageKeys;
-    int64_t most = stages < 16 ? 1 : stages / 3;
-    if (most > 64) most = stages / 8 > 64 ? stages / 8 : 64;
-    if (split > most) split = most;
-    pl.n_split = split > 1 ? int(split) : 1;
-    pl.n_parts = split > 1 ? units : 0;
+    int64_t parts = stages < 16 ? 1 : stages / 3;
+    if (parts > 64) parts = stages / 8 > 64 ? stages / 8 : 64;
+    if (parts > wave / units) parts = wave / units;
+    // Or as many CTAs of a cluster, which join their parts themselves: up to
+    // the portable eight, from two stages each and eight stages on, and as many
+    // as the GPU holds at once (clusters of two to eight fill 86.5% of its
+    // places or more; nine for 48 slices left some for a second wave, 65 us
+    // against 47).  The launch that this saves is worth twelve stages or so.
+    // Measured in a captured graph, us, cluster / join: 24 slices x 4999 keys of
+    // 64, 13 rows 14.0 / 15.0; 48 x 1000 of 96, 13 rows 10.5 / 13.1; 8 x 512 of
+    // 96 5.9 / 7.5 (whole); 4 x 9000 of 128, 20 rows 21.8 / 15.5; launched one
+    // by one, where a launch is the host's time: 48 x 25600 of 96, one row 46.6
+    // / 49.0; 8 x 4096 of 96 18.6 / 23.6.
+    int64_t c = stages < 8 ? 1 : int64_t(double(wave) * 0.865) / units;
+    if (c > 8) c = 8;
+    if (c > stages / 2) c = stages / 2;
+    if (c > 1 && stages * (parts - c) <= 12 * c * parts) {
+      pl.n_split = int(c);
+      pl.cluster = true;
+    } else if (parts > 1) {
+      pl.n_split = int(parts);
+      pl.n_parts = units;
+    }
   } else {
     // The units that do not fill a wave of the SMs run as 2..16 parts over
     // the key tiles where that ends the call sooner.  Measured on B200: a CTA
@@ -619,7 +702,18 @@ static safedit_status launch_rows(const CUtensorMap& tmK, const CUtensorMap& tmV
   const safedit_status st = set_smem(reinterpret_cast<const void*>(kern), RowsCfg<D>::SMEM);
   if (st != SAFEDIT_OK) return st;
   const dim3 grid{unsigned(p.n_split), unsigned(p.n_tiles), unsigned(BH)};
-  kern<<<grid, kRowThreads8, RowsCfg<D>::SMEM, s>>>(tmK, tmV, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kRowThreads8);
+  cfg.dynamicSmemBytes = RowsCfg<D>::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(p.n_split);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, tmK, tmV, p) != cudaSuccess) return SAFEDIT_ERR_CUDA;
   return after_launch(1);
 }
 
@@ -730,6 +824,7 @@ extern "C" safedit_status safedit_attn_subset_state8(const safedit_tensor* q, co
   p.n_tiles = pl.n_tiles;
   p.n_records = pl.n_records;
   p.dual = pl.dual;
+  p.cluster = pl.cluster;
   p.part = static_cast<float*>(d_workspace);
   p.status = status_ptr();
   if (!p.status) return SAFEDIT_ERR_CUDA;

@@ -43,10 +43,11 @@ struct State8Params {
   uint64_t wait_limit;
   // Schedule: units of query rows (n_tiles of them in a (b, h) slice).  Units
   // below n_full run whole; each later one as n_split parts over the keys,
-  // whose records (of `tile_rows` rows, see PartView) are joined afterwards.
+  // whose records (of `tile_rows` rows, see PartView) are joined afterwards, or,
+  // with few rows, as the n_split CTAs of a cluster (`cluster`), no records.
   // With at most 128 rows both query tiles of the tensor-core kernel hold the
   // same rows and take the key tiles in turn (`dual`, two records a part).
-  int n_full, n_split, unit_rows, tile_rows, n_tiles, dual;
+  int n_full, n_split, unit_rows, tile_rows, n_tiles, dual, cluster;
   float* part;
   int64_t n_records;
 };

@@ -352,20 +352,22 @@ def test_a_step_of_the_trajectory(kind):
     assert float((got - ref).norm() / ref.norm()) <= 2.0 ** -4 * 1.5
 
 
-@pytest.mark.parametrize("n", (1, 12, 40, 100, 300))
+@pytest.mark.parametrize("n, H, N", ((1, 300, 2000), (12, 300, 2000), (1, 44, 6000), (12, 44, 6000), (40, 3, 2000),
+                                     (100, 3, 2000), (300, 3, 2000)))
 @pytest.mark.parametrize("kind", CODES)
 @pytest.mark.parametrize("masked", (False, True))
-def test_waits_that_run_out_end_the_call(n, kind, masked):
+def test_waits_that_run_out_end_the_call(n, H, N, kind, masked):
     """With no time to wait every role gives up: reported, the device stays usable, and the next call is right.
-    (Few rows take 300 heads: a part then has more keys than a block's copies in flight hold, so that one waits.)"""
-    B, H, N, d, block = 1, 300 if n <= 32 else 3, 2000, 96, 64
+    (With few rows a block has more keys than its copies in flight hold, so that one waits: 300 heads whole, or the
+    keys of 44 heads over eight blocks each.)"""
+    B, d, block = 1, 96, 64
     st = state(B, H, N, d, kind, block, 1), state(B, H, N, d, kind, block, 2)
     q = rows((B, H, n, d), BF, 3)
     pad = None
     if masked:
         pad = padded(B, N)
         pad[:, 5::7] = -math.inf
-        pad[:, 1500:] = -math.inf
+        pad[:, N - 500:] = -math.inf
     first = run(q, st, block, pad=pad)
     old = sd().safedit_debug_set_wait_limit_ns(0)
     try:
@@ -451,3 +453,33 @@ def test_scales_of_masked_blocks_count_for_nothing(n, value, kind):
     out, A = attend(q, st, block, None, pad)
     ks[:, :, dead], vs[:, :, dead] = value, value
     close(run(q, st, block, pad=pad), out, A)
+
+
+@pytest.mark.parametrize("n", (1, 9, 32))
+@pytest.mark.parametrize("H, N", ((3, 300), (3, 511), (3, 520), (1, 9000), (44, 700), (60, 1500), (110, 1030), (230, 600)))
+def test_few_rows_whole_in_clusters_and_in_parts(n, H, N):
+    """Short and long states, few slices and many: keys whole, over two to eight blocks that join them, and in parts; a
+    row without a key in one batch, a bad index, masked keys over whole parts."""
+    d, block = (64, 96, 128)[(n + N) % 3], 16
+    kind = "int8" if n % 2 else "e4m3"
+    st = state(2, H, N, d, kind, block, 1), state(2, H, N, d, kind, block, 2)
+    pad = padded(2, N)
+    pad[0, N // 3:] = -math.inf
+    pad[1, : N // 2] = -math.inf
+    idx = torch.randperm(40, generator=torch.Generator().manual_seed(n))[:n].to(torch.int32).to(DEV)
+    q = rows((2, H, 40, d), BF, 3)
+    close(run(q, st, block, idx=idx, pad=pad), *attend(q, st, block, idx, pad))
+    out = run(q, st, block, idx=idx)
+    close(out, *attend(q, st, block, idx, None))
+    assert torch.equal(out, run(q, st, block, idx=idx))
+    pad[1] = -math.inf
+    idx[n // 2] = 40
+    got = torch.full((2, H, n, d), 7.0, dtype=BF, device=DEV)
+    sd().safedit_attn_subset_state8(q, st[0][0], st[0][1], st[1][0], st[1][1], block, idx, n, pad, 0.0, got, 0,
+                                    workspace(2, H, n, N, d))
+    expect_status(sd().ERR_INDEX)
+    keep = [r for r in range(n) if r != n // 2]
+    assert bool((got[:, :, n // 2] == 7.0).all())
+    assert bool((got[1, :, keep] == 0.0).all())
+    ref, A = attend(q, st, block, idx[keep], pad)
+    close(got[:1, :, keep], ref[:1], A[:1])

@@ -192,7 +192,7 @@ def test_attention_workspace_size(sd):
                 (1 << 40, 1 << 40, 1, 1, 64), (1, 1, 1 << 40, 1, 64), (1, 1, 1, 1 << 40, 64), (-1, 1, 1, 1, 64)):
         assert ws(*bad) == 0
     assert ws(1, 1, 1, 1, 64) == 0      # one key: nothing to split
-    assert ws(2, 24, 1, 25600, 96) > 0  # one row: the keys go over the SMs
+    assert ws(1, 1, 1, 25600, 96) > 0   # one row of one slice: the keys go over the SMs
 
 
 def test_other_calls_refuse_code_types(sd):
