@@ -582,10 +582,10 @@ static int state8_sms() {
 }
 
 // Rows of a slice up to which the warp-level kernel is taken.  Measured, us,
-// warp-level / tensor-core kernel: 48 slices x 25600 keys of 96: 16 rows 59 /
-// 123, 32 rows 109 / 124, 48 rows 140 / 126; x 4096 keys: 16 rows 27 / 36, 32
-// rows 40 / 36; 32 slices x 16384 keys of 128: 32 rows 84 / 82; 4 slices: 32
-// rows 25 / 32.
+// warp-level / tensor-core kernel: 48 slices x 25600 keys of 96: 16 rows 64 /
+// 120, 32 rows 108 / 118, 48 rows 148 / 122; x 4096 keys: 16 rows 23 / 33, 32
+// rows 30 / 33, 48 rows 37 / 36; 32 slices x 16384 keys of 128: 32 rows 70 /
+// 76, 48 rows 91 / 76; 4 slices x 4096 of 96: 32 rows 19 / 25.
 constexpr int64_t kFewRows = 32;
 
 static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int sms) {
