@@ -39,6 +39,7 @@ struct RowsCfg {
   static constexpr int CTAS = D == 64 ? 4 : 3;       // on an SM
   static constexpr int SMEM = 1024 + NST * 2 * TILE;
   static_assert(NST * 2 * TILE >= (kRowWarps + 1) * 16 * D * 4, "the warps' results fit the ring");
+  static_assert(D % 2 == 0, "and the cluster reads the joined rows by pairs from a multiple of 8 bytes on");
 };
 constexpr uint64_t kRowsDrainNs = 1000000000ull;
 
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   constexpr int NT = D / 16;       // tiles of 16 output columns
   constexpr int ROWS = 8 * NQ;     // query rows of the CTA
   constexpr bool CLEAR = PAD && E4M3;  // codes of masked keys may be NaN
-  extern __shared__ uint8_t rows_smem[];
+  extern __shared__ __align__(16) uint8_t rows_smem[];
   __shared__ uint64_t full[C::NST], empty[C::NST];
   __shared__ int abort_word;
   __shared__ float sm_m[kRowWarps][ROWS], sm_l[kRowWarps][ROWS], sm_range[kRowWarps][2];
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   __syncthreads();
   // each warp's scaled output to the ring (its copies have all landed), added
   // in the warps' order
-  float* const sm_part = reinterpret_cast<float*>(rows_smem);
+  float* const sm_part = reinterpret_cast<float*>(rows_smem + (ring - smem_u32(rows_smem)));
   if (warp < kRowWarps) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
