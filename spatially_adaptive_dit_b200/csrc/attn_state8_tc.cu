@@ -64,7 +64,7 @@ struct TcCfg {
   static constexpr int OFF_PAD = OFF_FACT + ((NF * 8 * 12 + 15) / 16) * 16;
   static constexpr int OFF_LIVE = OFF_PAD + NF * 128 * 4;
   static constexpr int OFF_TOP = OFF_LIVE + LIVE_WORDS * 4;  // the largest pad
-  static constexpr int OFF_DEAD = OFF_TOP + 4;               // a byte for each 32 pads of a slot: one is -inf
+  static constexpr int OFF_DEAD = OFF_TOP + 4;               // for each slot: a key of the tile is masked
   static constexpr int SMEM_PLAIN = 1024 + OFF_PAD;
   static constexpr int SMEM_PAD = 1024 + OFF_DEAD + NF * 4;
   static_assert(SMEM_PAD <= 232448, "shared memory");
@@ -784,73 +784,74 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // products took the weights of tile `it - NS` from both query tiles, so
     // nobody reads that slot any more, and tile `it + 1` takes it.  Their loads
     // go out a step before.
-    float next_ks = 0.f, next_vs = 1.f, next_pad[2] = {0.f, 0.f}, next_pvs[2] = {1.f, 1.f};
+    // Warp 8 does it: a lane holds the scales of group lane % 8 and the pads of
+    // keys 4 lane .. 4 lane + 3, so it knows each group's live keys; scales of a
+    // group without one count for nothing, whatever they are.
+    float next_ks = 0.f, next_vs = 1.f;
+    float4 next_pad = make_float4(0.f, 0.f, 0.f, 0.f);
     auto fetch = [&](int kt) {
-      const int key = kt * C::BN + tid * 16;
-      if (tid < 8 && key < p.Nk) {
+      const int key = kt * C::BN + (lane & 7) * 16;
+      if (key < p.Nk) {
         next_ks = __ldg(ksb + (key >> p.block_log2));
         next_vs = __ldg(vsb + (key >> p.block_log2));
       }
       if constexpr (PAD) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = tid + e * kTcWidenThreads, k = kt * C::BN + c;
-          if (c < C::BN) next_pad[e] = k < p.Nk ? __ldg(padb + k) : -INFINITY;
-          if (c < C::BN && k < p.Nk) next_pvs[e] = __ldg(vsb + (k >> p.block_log2));
+        const int k = kt * C::BN + 4 * lane;
+        next_pad = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (k + 4 <= p.Nk) {
+          next_pad = __ldg(reinterpret_cast<const float4*>(padb + k));
+        } else {
+          if (k < p.Nk) next_pad.x = __ldg(padb + k);
+          if (k + 1 < p.Nk) next_pad.y = __ldg(padb + k + 1);
+          if (k + 2 < p.Nk) next_pad.z = __ldg(padb + k + 2);
         }
       }
     };
     auto publish = [&](int kt, int slot) {
-      if (tid < 8) {
-        const int key = kt * C::BN + tid * 16;
-        float ks = 0.f, lv = 0.f;
-        if (key < p.Nk) {
-          ks = next_ks;
-          lv = __log2f(next_vs);
-          const bool bad = !(ks >= 0.f && ks < INFINITY && next_vs > 0.f && next_vs < INFINITY);
-          bool used = true;  // a key of the group that is not masked
-          if constexpr (PAD) {  // looked up where it makes a difference
-            if (bad || fabsf(lv) > 0.5f * kScaleSpread) {
-              used = false;
-              for (int e = 0; e < 16 && key + e < p.Nk; ++e) used |= __ldg(padb + key + e) != -INFINITY;
-            }
-          }
-          if (!used) {
-            ks = 0.f, lv = 0.f;
-          } else if (bad) {
-            set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
-          } else {
-            lv_lo = fminf(lv_lo, lv);
-            lv_hi = fmaxf(lv_hi, lv);
-          }
+      bool used = kt * C::BN + (lane & 7) * 16 < p.Nk;
+      if constexpr (PAD) {
+        const uint32_t live = __ballot_sync(0xffffffffu, next_pad.x != -INFINITY || next_pad.y != -INFINITY ||
+                                                             next_pad.z != -INFINITY || next_pad.w != -INFINITY);
+        used = (live >> (4 * (lane & 7)) & 15u) != 0u;
+      }
+      float ks = 0.f, lv = 0.f;
+      if (used) {
+        ks = next_ks;
+        lv = __log2f(next_vs);
+        if (!(ks >= 0.f && ks < INFINITY && next_vs > 0.f && next_vs < INFINITY)) {
+          set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
+        } else {
+          lv_lo = fminf(lv_lo, lv);
+          lv_hi = fmaxf(lv_hi, lv);
         }
-        const uint32_t f = sb + uint32_t(C::OFF_FACT + slot * 96 + tid * 4);
+      }
+      if (lane < 8) {
+        const uint32_t f = sb + uint32_t(C::OFF_FACT + slot * 96 + lane * 4);
         sts32(f, ks);
         sts32(f + 32u, lv);
         sts32(f + 64u, ex2_approx(-lv));
       }
       if constexpr (PAD) {
+        float pd[4] = {next_pad.x, next_pad.y, next_pad.z, next_pad.w};
+        const float lk = far_pad != 0.f ? 0.f : __shfl_sync(0xffffffffu, lv, lane >> 2);
+        bool dead = false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = tid + e * kTcWidenThreads;
-          if (c < C::BN) {
-            const float v = pad_log2(next_pad[e]);
-            sts32(sb + uint32_t(C::OFF_PAD + slot * 512 + c * 4),
-                  far_pad != 0.f || v == -INFINITY ? v : v + __log2f(next_pvs[e]));
-            if constexpr (E4M3) {  // a whole warp: 32 keys
-              const bool any = __any_sync(0xffffffffu, v == -INFINITY);
-              if (lane == 0)
-                asm volatile("st.shared.u8 [%0], %1;" ::"r"(sb + uint32_t(C::OFF_DEAD + slot * 4 + c / 32)),
-                             "r"(uint32_t(any))
-                             : "memory");
-            }
-          }
+        for (int e = 0; e < 4; ++e) {
+          pd[e] = pad_log2(pd[e]);
+          dead |= pd[e] == -INFINITY;
+          if (pd[e] != -INFINITY) pd[e] += lk;
+        }
+        sts128(sb + uint32_t(C::OFF_PAD + slot * 512 + lane * 16), __float_as_uint(pd[0]), __float_as_uint(pd[1]),
+               __float_as_uint(pd[2]), __float_as_uint(pd[3]));
+        if constexpr (E4M3) {
+          dead = __any_sync(0xffffffffu, dead);
+          if (lane == 0) sts32(sb + uint32_t(C::OFF_DEAD + slot * 4), dead ? 1.f : 0.f);
         }
       }
     };
     bool ok = true;
     int slot = 0, kt = next_live(k_lo);
-    if (n_live > 0) {
+    if (warp == 8 && n_live > 0) {
       fetch(kt);
       publish(kt, 0);
     }
@@ -860,16 +861,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t ph = uint32_t((it / C::NS) & 1) ^ 1u;
       const int kt1 = next_live(kt + 1), slot1 = slot + 1 == C::NF ? 0 : slot + 1;
       const bool more = it + 1 < n_live;
-      if (more) fetch(kt1);
+      if (warp == 8 && more) fetch(kt1);
       bool dead = false;  // a key of this tile is masked
-      if constexpr (PAD && E4M3) dead = __float_as_uint(lds32(sb + uint32_t(C::OFF_DEAD + slot * 4))) != 0u;
+      if constexpr (PAD && E4M3) dead = lds32(sb + uint32_t(C::OFF_DEAD + slot * 4)) != 0.f;
       for (int kv = 0; ok && kv < 2; ++kv) {
         const int n = 2 * it + kv, raw = n % C::NR;
         ok = wait_warp(BAR(RAW_FULL + raw), uint32_t((n / C::NR) & 1), ctl) &&
              wait_warp(BAR((kv ? V_EMPTY : K_EMPTY) + s), ph, ctl);
         const uint32_t to = sb + uint32_t((kv ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES);
         if (ok) {
-          if (kv && more) publish(kt1, slot1);
+          if (warp == 8 && kv && more) publish(kt1, slot1);
           widen(sb + uint32_t(C::OFF_RAW + raw * C::RAW_BYTES), to);
         }
         if constexpr (PAD && E4M3) {

@@ -1,0 +1,71 @@
+"""Attention over the 8-bit state where the scales of V, the pads and the codes are of every size the interface admits.
+
+Tolerance, per element, with A = sum_j p_j |v_j| and S = max_j(p_j) sum_j |v_j| in fp64:
+  |got - out| <= 2^-8 |out| + (2^-11 + 2^-12) A + 2^-23 S
+  - the result is rounded once to bf16: half a step, 2^-8 of the value;
+  - every weight is rounded to f16 or finer (half a step, 2^-11 relative): at most 2^-11 A;
+  - f16's steps stop shrinking at 2^-14, where half a step is 2^-25 of the largest p_j vs_j, and the scales vs of the
+    keys in use lie within 2^2 of one another: 2^-23 max(p) of each |v|;
+  - scores of N(0,1) rows: under 2^-12 A (as in the tests of the ordinary range).
+Every term goes by the element's own values, so a row or a channel that lost its share of the sum is seen whatever
+the others hold.
+"""
+import math
+
+import pytest
+import torch
+
+from tests.gpu_util import sd
+from tests.test_gpu_attn_state8 import BF, dense, padded, run, state
+from tests.test_gpu_rope import rows
+
+pytestmark = pytest.mark.gpu
+# rows of a call: one, two tiles of the kernel for few rows, both query tiles on the same rows, units of 256
+COUNTS = (1, 12, 40, 300)
+
+
+def attended(q, st, block, pad=None, scale=None):
+    """(out, A, S) in fp64."""
+    (k8, ks), (v8, vs) = st
+    k, v = dense(k8, ks, block), dense(v8, vs, block)
+    t = q.double().cpu() @ k.transpose(2, 3) * (q.shape[-1] ** -0.5 if scale is None else scale)
+    if pad is not None:
+        dead = pad.cpu() == -math.inf
+        t = t + pad.double().cpu()[:, None, None, :]
+        t = torch.where(dead[:, None, None, :], torch.full_like(t, -math.inf), t)
+        v = torch.where(dead[:, None, :, None], torch.zeros_like(v), v)
+    p = torch.softmax(t, -1)
+    return p @ v, p @ v.abs(), p.amax(-1, keepdim=True) * v.abs().sum(2, keepdim=True)
+
+
+def bound(out, A, S):
+    return 2.0 ** -8 * out.abs() + (2.0 ** -11 + 2.0 ** -12) * A + 2.0 ** -23 * S
+
+
+def close(got, out, A, S):
+    err, most = (got.double().cpu() - out).abs(), bound(out, A, S)
+    assert bool((err <= most).all()), f"worst error/bound {float((err / most.clamp_min(1e-300)).max()):.3g}"
+
+
+def scaled(B, H, N, d, kind, block, seed, power):
+    """Codes and scales of N(0, 4^power) rows."""
+    codes, scales = state(B, H, N, d, kind, block, seed)
+    return codes, scales * 2.0 ** power
+
+
+@pytest.mark.parametrize("n", COUNTS)
+@pytest.mark.parametrize("kind", ("e4m3", "int8"))
+@pytest.mark.parametrize("live, masked", ((-30.0, 2.0 ** 30), (30.0, 2.0 ** -40), (0.0, 2.0 ** 31)))
+def test_masked_blocks_beside_scales_of_another_size(n, kind, live, masked):
+    """A masked block's scales count for nothing whatever they are: ordinary values too, in tiles with live keys."""
+    B, H, N, d, block = 1, 2, 600, 64, 16
+    st = state(B, H, N, d, kind, block, 1), scaled(B, H, N, d, kind, block, 2, live)
+    q = rows((B, H, n, d), BF, 3)
+    pad = padded(B, N)
+    dead = [0, 3, 4, 17, 24, 25, 26, 27, 28, 29, 30, 31, 37]
+    for i in dead:
+        pad[:, i * block: (i + 1) * block] = -math.inf
+    want = attended(q, st, block, pad)
+    for _, f in st:
+        f[:, :, dead] = masked
+    close(run(q, st, block, pad=pad), *want)
