@@ -436,7 +436,8 @@ safedit_status safedit_state8_store(const safedit_tensor *src,
  * and those of one (b, h) slice of V within a factor of 2^64 of each other;
  * otherwise SAFEDIT_ERR_INVALID_ARG is set and the rows are unspecified.
  * A row whose every key is masked sets SAFEDIT_ERR_MASKED_ROW and gets zeros.
- * out must not overlap an input.
+ * A query row with a NaN comes out as NaN, with no status; the other rows do
+ * not depend on it.  out must not overlap an input.
  *
  * d_workspace / workspace_bytes as in safedit_attn_subset_ws: at least
  * safedit_attn_subset_state8_workspace_size(...) bytes for this call on the

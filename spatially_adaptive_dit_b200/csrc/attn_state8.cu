@@ -426,8 +426,10 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   float mx = -INFINITY, lx = 0.f;  // of row threadIdx.x
   if (threadIdx.x < ROWS) {
     for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, sm_m[w][threadIdx.x]);
-    for (int w = 0; w < kRowWarps; ++w)
-      if (sm_m[w][threadIdx.x] != -INFINITY) lx = fmaf(ex2_approx(sm_m[w][threadIdx.x] - mx), sm_l[w][threadIdx.x], lx);
+    for (int w = 0; w < kRowWarps; ++w) {  // (scores of NaN leave m at -inf and l at NaN, which stays)
+      const float mw = sm_m[w][threadIdx.x];
+      lx = fmaf(mw == -INFINITY ? 0.f : ex2_approx(mw - mx), sm_l[w][threadIdx.x], lx);
+    }
   }
   if (p.cluster) {
     // ---- the parts joined by the cluster's CTAs: each takes its share of the

@@ -69,3 +69,31 @@ def test_masked_blocks_beside_scales_of_another_size(n, kind, live, masked):
     for _, f in st:
         f[:, :, dead] = masked
     close(run(q, st, block, pad=pad), *want)
+
+
+# (rows, heads, keys): whole, over a cluster's blocks, in parts; both query tiles on the same rows whole and in parts;
+# units of 256 rows whole and with the last ones in parts
+PLANS = ((1, 2, 300), (12, 2, 300), (1, 3, 4000), (9, 40, 3000), (1, 1, 30000), (20, 1, 30000), (40, 2, 200),
+         (100, 2, 6000), (300, 2, 600), (300, 2, 9000))
+
+
+@pytest.mark.parametrize("n, H, N", PLANS)
+@pytest.mark.parametrize("kind", ("e4m3", "int8"))
+@pytest.mark.parametrize("masked", (False, True))
+def test_a_query_row_of_nan(n, H, N, kind, masked):
+    """It comes out as NaN with no status in every plan, and the other rows as if it were not there."""
+    d, block = 96, 64
+    st = state(1, H, N, d, kind, block, 1), state(1, H, N, d, kind, block, 2)
+    q = rows((1, H, n, d), BF, 3)
+    pad = None
+    if masked:
+        pad = padded(1, N)
+        pad[:, N // 5: N // 3] = -math.inf
+        pad[:, N - N // 4:] = -math.inf
+    want = attended(q, st, block, pad)
+    bad = n // 2
+    q[:, :, bad, 5] = math.nan
+    got = run(q, st, block, pad=pad)
+    assert bool(got[:, :, bad].isnan().all())
+    keep = [r for r in range(n) if r != bad]
+    close(got[:, :, keep], *(x[:, :, keep] if x.shape[2] == n else x for x in want))
