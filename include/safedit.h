@@ -432,9 +432,11 @@ safedit_status safedit_state8_store(const safedit_tensor *src,
  *
  * A key with key_pad == -inf carries no weight whatever its codes and scales
  * hold.  The other keys' codes must not be NaN (safedit_state8_store writes
- * none), their scales must be finite, k_scale >= 0, v_scale > 0,
- * and those of one (b, h) slice of V within a factor of 2^64 of each other;
- * otherwise SAFEDIT_ERR_INVALID_ARG is set and the rows are unspecified.
+ * none), their pads neither NaN nor +inf, their scales must be finite,
+ * k_scale >= 0, v_scale > 0, and those of one (b, h) slice of V within a
+ * factor of 2^64 of each other; otherwise SAFEDIT_ERR_INVALID_ARG is set and
+ * the rows are unspecified.  (NaN codes and pads are known by the rows that
+ * they make NaN, so a finite query row has to be among the call's.)
  * A row whose every key is masked sets SAFEDIT_ERR_MASKED_ROW and gets zeros.
  * A query row with a NaN comes out as NaN, with no status; the other rows do
  * not depend on it.  out must not overlap an input.

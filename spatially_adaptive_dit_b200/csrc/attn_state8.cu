@@ -466,8 +466,10 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
       }
       if (ls == 0.f && c == 0) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
       const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      a0 *= inv, a1 *= inv;
+      if (a0 != a0 || a1 != a1) report_nan(p, b, h, qi, D);
       const int64_t orow = p.out_scattered ? int64_t(qi) : int64_t(r);
-      *reinterpret_cast<uint32_t*>(p.out + b * p.o_sb + h * p.o_sh + orow * p.o_sr + c) = pack_bf16x2(a0 * inv, a1 * inv);
+      *reinterpret_cast<uint32_t*>(p.out + b * p.o_sb + h * p.o_sh + orow * p.o_sr + c) = pack_bf16x2(a0, a1);
     }
     rows_cluster_sync();  // nobody leaves while another still reads it
     return;
@@ -491,9 +493,10 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
     const float ls = sm_l[0][rr];
     if (ls == 0.f && c == 0) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
     const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    const float a0 = joined(rr * D + c) * inv, a1 = joined(rr * D + c + 1) * inv;
+    if (a0 != a0 || a1 != a1) report_nan(p, b, h, qi, D);
     const int64_t orow = p.out_scattered ? int64_t(qi) : int64_t(r);
-    *reinterpret_cast<uint32_t*>(p.out + b * p.o_sb + h * p.o_sh + orow * p.o_sr + c) =
-        pack_bf16x2(joined(rr * D + c) * inv, joined(rr * D + c + 1) * inv);
+    *reinterpret_cast<uint32_t*>(p.out + b * p.o_sb + h * p.o_sh + orow * p.o_sr + c) = pack_bf16x2(a0, a1);
   }
 }
 
@@ -564,8 +567,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_state8_join_kernel(const
     if (hi - lo > kScaleSpread) set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
     if (l == 0.f) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
   }
+  sum = l == 0.f ? 0.f : sum / l;
+  if (sum != sum) report_nan(p, b, h, qi, D);
   const int64_t orow = p.out_scattered ? int64_t(qi) : int64_t(r);
-  p.out[b * p.o_sb + h * p.o_sh + orow * p.o_sr + threadIdx.x] = __float2bfloat16_rn(l == 0.f ? 0.f : sum / l);
+  p.out[b * p.o_sb + h * p.o_sh + orow * p.o_sr + threadIdx.x] = __float2bfloat16_rn(sum);
 }
 
 // ------------------------------------------------------------- plan

@@ -108,6 +108,17 @@ __device__ __forceinline__ float query_factor(uint32_t max_bits, float scale, fl
   return __uint_as_float(uint32_t(127 + f) << 23);
 }
 
+// A row came out as NaN: where its query row is finite, a NaN among the codes
+// (or the pads) did it.  Looked at where results leave, so that the loops over
+// keys need not look at every code.
+__device__ __forceinline__ void report_nan(const State8Params& p, int b, int h, int qi, int D) {
+  const uint16_t* row = reinterpret_cast<const uint16_t*>(p.q + b * p.q_sb + h * p.q_sh + int64_t(qi) * p.q_sr);
+#pragma unroll 1
+  for (int c = 0; c < D; ++c)
+    if ((__ldg(row + c) & 0x7F80u) == 0x7F80u) return;
+  set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
+}
+
 // A part's record: O [rows][D] unnormalised, (m, l) [rows], and the smallest
 // and largest log2 vs that it met (of all records behind one another).
 struct PartView {

@@ -120,6 +120,16 @@ __device__ __forceinline__ void sts32(uint32_t at, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
+// The larger ones of two pairs of bf16, NaN where one is.
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ bool nan_bf16x2(uint32_t v) {
+  return (v & 0x7FFFu) > 0x7F80u || (v & 0x7FFF0000u) > 0x7F800000u;
+}
+
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -549,14 +559,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           __syncwarp();
           __nv_bfloat16* const ob = p.out + b * p.o_sb + h * p.o_sh;
+          uint32_t top[2] = {0u, 0u};  // NaN where the lane sees one on its way
 #pragma unroll
           for (int i = 0; i < UNITS; ++i) {
             const int u = lane + 32 * i, row = u / UNITS, c = u - row * UNITS;
             const int qi = __shfl_sync(0xffffffffu, my_q, row);
             const int64_t at = p.out_scattered ? int64_t(qi) : int64_t(row0 + (rr & ~31) + row);
-            if (qi >= 0)
-              *reinterpret_cast<uint4*>(ob + at * p.o_sr + c * 8) = lds128(stage + uint32_t(row * PITCH + c * 16));
+            const uint4 v = lds128(stage + uint32_t(row * PITCH + c * 16));
+            if constexpr (E4M3) {
+              top[0] = max_nan_bf16x2(max_nan_bf16x2(top[0], v.x), v.y);
+              top[1] = max_nan_bf16x2(max_nan_bf16x2(top[1], v.z), v.w);
+            }
+            if (qi >= 0) *reinterpret_cast<uint4*>(ob + at * p.o_sr + c * 8) = v;
           }
+          bool nan = inv != inv;  // of scores; a NaN code of V leaves the sum alone (int8 has none)
+          if constexpr (E4M3) {
+            if (__any_sync(0xffffffffu, nan_bf16x2(top[0]) || nan_bf16x2(top[1]))) {  // each lane its own row
+#pragma unroll 1
+              for (int c = 0; c < D / 2; ++c) nan |= nan_bf16x2(__float_as_uint(lds32(mine + uint32_t(c * 4))));
+            }
+          }
+          if (nan && live) report_nan(p, b, h, my_q, D);
         } else {
           const PartView pv = part_view(p, dual ? 2 * rest + t : rest, D);
           if (live) {

@@ -97,3 +97,26 @@ def test_a_query_row_of_nan(n, H, N, kind, masked):
     assert bool(got[:, :, bad].isnan().all())
     keep = [r for r in range(n) if r != bad]
     close(got[:, :, keep], *(x[:, :, keep] if x.shape[2] == n else x for x in want))
+
+
+@pytest.mark.parametrize("n, H, N", PLANS)
+@pytest.mark.parametrize("where", ("k", "v", "k beside pads", "v beside pads", "pad", "pad of inf"))
+def test_nan_codes_and_pads_are_reported(n, H, N, where):
+    """One NaN code of a key that is not masked, or one pad that is no number, in every plan; under -inf it is nothing."""
+    d, block = 96, 64
+    st = state(1, H, N, d, "e4m3", block, 1), state(1, H, N, d, "e4m3", block, 2)
+    q = rows((1, H, n, d), BF, 3)
+    pad = None
+    if "pad" in where:
+        pad = padded(1, N)
+        pad[:, N // 5: N // 3] = -math.inf
+    at = N // 2
+    if where.startswith("pad"):
+        pad[0, at] = math.inf if "inf" in where else math.nan
+    else:
+        st["kv".index(where[0])][0].view(torch.uint8)[0, 0, at, 11] = 0xFF
+    run(q, st, block, pad=pad, status=sd().ERR_INVALID_ARG)
+    if pad is not None:
+        pad[0, at] = -math.inf
+        clean = [(c.float().nan_to_num(0.0), f) for c, f in st]
+        close(run(q, st, block, pad=pad), *attended(q, clean, block, pad))
