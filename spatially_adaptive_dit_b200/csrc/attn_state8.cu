@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   // queries 2 t and 2 t + 1 of each tile of eight
   float m[NQ][2], l[NQ][2];
   float lv_lo = INFINITY, lv_hi = -INFINITY;
+  float base = NAN;  // of this warp's V scales, NaN before the first
   bool ok = true;
   float o[NQ][NT][4];
 #pragma unroll
@@ -251,11 +252,13 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
       if constexpr (PAD) live = __any_sync(0xffffffffu, pad[0] != -INFINITY || pad[1] != -INFINITY);
       if (live) {
         const uint32_t kt = ring + uint32_t(i * 2 * C::TILE), vt = kt + uint32_t(C::TILE);
-        const float lv = __log2f(vs);
+        float lv = __log2f(vs);
         // finite, ks >= 0, vs > 0, by their bits
         bad |= __float_as_uint(ks) >= 0x7F800000u || __float_as_uint(vs) - 1u >= 0x7F7FFFFFu;
         lv_lo = fminf(lv_lo, lv);
         lv_hi = fmaxf(lv_hi, lv);
+        if (base != base) base = scale_base(lv);
+        lv -= base;
         float s[NQ][4];
 #pragma unroll
         for (int q = 0; q < NQ; ++q) s[q][0] = s[q][1] = s[q][2] = s[q][3] = 0.f;
@@ -381,11 +384,14 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   if (__syncthreads_or(!ok) && !p.cluster) return;
 
   // ---- the warps' results joined in shared memory
+  float up = 1.f;
   if (warp < kRowWarps) {
+    if (base != base) base = 0.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        up = leave_base(base, m[q][e], l[q][e]);
         l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 4);
         l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 8);
         l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 16);
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
         float mx = -INFINITY;
 #pragma unroll
         for (int v = 0; v < kRowWarps; ++v) mx = fmaxf(mx, sm_m[v][r]);
-        const float f = m[q][e] == -INFINITY ? 0.f : ex2_approx(m[q][e] - mx);
+        const float f = m[q][e] == -INFINITY ? 0.f : ex2_approx(m[q][e] - mx) * up;
         float* row = sm_part + (warp * ROWS + r) * D;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {

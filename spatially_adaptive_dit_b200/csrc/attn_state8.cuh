@@ -7,13 +7,16 @@
 //   out = sum_j p_j vs_j v8_j / sum_j p_j
 //
 // Scales never touch a code: ks goes into the score's factor, and vs into the
-// exponent of the weight w_j = 2^(t_j + log2 vs_j - m), m the running maximum
-// of t_j + log2 vs_j.  So the weights that the tensor cores multiply with the
-// codes are at most 2^8 (with the lazy rescale) whatever the scales' range,
-// and f16 holds them to 2^-12; the row sum is sum_j w_j / vs_j in fp32.  Codes
-// of both types are exact in f16, as is a bf16 query row after a power of two
-// has brought its largest element to 2^12 (elements 2^-29 below it lose bits:
-// 2^-36 of the row's largest), so the f16 weights are the only rounding.
+// exponent of the weight w_j = 2^(t_j + lv_j - m), lv = log2 vs - base, m the
+// running maximum of t_j + lv_j.  So the weights that the tensor cores multiply
+// with the codes are at most 2^8 (with the lazy rescale) whatever the scales'
+// range, and f16 holds them to 2^-11; the row sum is sum_j w_j 2^-lv_j in fp32.
+// The base, the first scale in use to the nearest power of two, comes back with
+// the result.  It keeps lv small: a far pad absorbs it as it does the score, and
+// the sum must neither overflow nor vanish at scales near the ends of fp32.
+// Codes of both types are exact in f16, as is a bf16 query row after a power of
+// two has brought its largest element to 2^12 (elements 2^-29 below it lose
+// bits: 2^-36 of the row's largest), so the f16 weights are the only rounding.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -106,6 +109,18 @@ __device__ __forceinline__ float query_factor(uint32_t max_bits, float scale, fl
   f = f > 126 ? 126 : f;
   undo = scale * __uint_as_float(uint32_t(127 - f) << 23);
   return __uint_as_float(uint32_t(127 + f) << 23);
+}
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(float e) { return __uint_as_float(uint32_t(127 + int(e)) << 23); }
+// The base of V scales from the log2 of the first one in use.
+__device__ __forceinline__ float scale_base(float lv) { return fminf(fmaxf(rintf(lv), -120.f), 120.f); }
+// Sums (m, l) relative to a base -> without it, and the factor of O that goes with
+// it: large bases leave by m and l and small ones by O, so neither overflows.
+__device__ __forceinline__ float leave_base(float base, float& m, float& l) {
+  m += fmaxf(base, 0.f);
+  l *= pow2(-fmaxf(base, 0.f));
+  return pow2(fminf(base, 0.f));
 }
 
 // A row came out as NaN: where its query row is finite, a NaN among the codes

@@ -61,7 +61,8 @@ struct TcCfg {
   static constexpr int OFF_BAR = OFF_RAW + NR * RAW_BYTES;
   static constexpr int N_BARS = 1 + 4 * NS + NR + 2 + 4 + 2;
   static constexpr int OFF_FACT = OFF_BAR + ((N_BARS * 8 + 8 + 15) / 16) * 16;
-  static constexpr int OFF_PAD = OFF_FACT + ((NF * 8 * 12 + 15) / 16) * 16;
+  static constexpr int OFF_BASE = OFF_FACT + NF * 8 * 12;  // of the V scales
+  static constexpr int OFF_PAD = OFF_BASE + 16;
   static constexpr int OFF_LIVE = OFF_PAD + NF * 128 * 4;
   static constexpr int OFF_TOP = OFF_LIVE + LIVE_WORDS * 4;  // the largest pad
   static constexpr int OFF_DEAD = OFF_TOP + 4;               // for each slot: a key of the tile is masked
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(BAR(O_FULL), 1);
     mbar_init(BAR(DRAIN), 1);
     *abort_flag = 0;
+    sts32(sb + uint32_t(C::OFF_BASE), 0.f);
     mbar_fence_init();
   }
   if (warp == 11) {
@@ -531,8 +533,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         const bool live = my_q >= 0;
         const bool empty = l_run == 0.f;  // O may never have been written
+        const float base = lds32(sb + uint32_t(C::OFF_BASE));
         if (live && whole && empty) set_status(p.status, SAFEDIT_ERR_MASKED_ROW);
-        const float inv = empty ? 0.f : 1.f / l_run;
+        const float inv = empty ? 0.f : pow2(base) / l_run;
         // Rows leave through shared memory (the query tiles', free by now), so
         // that a warp's stores run along rows: bf16 rows at once, a part's
         // fp32 rows half a row at a time.  Rows are 16 bytes apart from a
@@ -582,6 +585,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (nan && live) report_nan(p, b, h, my_q, D);
         } else {
           const PartView pv = part_view(p, dual ? 2 * rest + t : rest, D);
+          const float up = leave_base(base, m_run, l_run);
           if (live) {
             pv.ml[rr * 2] = m_run;
             pv.ml[rr * 2 + 1] = l_run;
@@ -595,8 +599,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                sts128(mine + uint32_t(c * 4 + e * 16), empty ? 0u : r[4 * e], empty ? 0u : r[4 * e + 1],
-                       empty ? 0u : r[4 * e + 2], empty ? 0u : r[4 * e + 3]);
+              {
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = empty ? 0u : __float_as_uint(__uint_as_float(r[4 * e + k]) * up);
+                sts128(mine + uint32_t(c * 4 + e * 16), o[0], o[1], o[2], o[3]);
+              }
             }
             __syncwarp();
 #pragma unroll
@@ -812,6 +820,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // group without one count for nothing, whatever they are.
     float next_ks = 0.f, next_vs = 1.f;
     float4 next_pad = make_float4(0.f, 0.f, 0.f, 0.f);
+    float base = NAN;  // of the V scales, NaN before the first in use
     auto fetch = [&](int kt) {
       const int key = kt * C::BN + (lane & 7) * 16;
       if (key < p.Nk) {
@@ -848,6 +857,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           lv_hi = fmaxf(lv_hi, lv);
         }
       }
+      const uint32_t in_use = __ballot_sync(0xffffffffu, used) & 255u;
+      if (base != base && in_use != 0u) {
+        base = scale_base(__shfl_sync(0xffffffffu, lv, __ffs(in_use) - 1));
+        if (lane == 0) sts32(sb + uint32_t(C::OFF_BASE), base);
+      }
+      if (used) lv -= base;
       if (lane < 8) {
         const uint32_t f = sb + uint32_t(C::OFF_FACT + slot * 96 + lane * 4);
         sts32(f, ks);

@@ -120,3 +120,36 @@ def test_nan_codes_and_pads_are_reported(n, H, N, where):
         pad[0, at] = -math.inf
         clean = [(c.float().nan_to_num(0.0), f) for c, f in st]
         close(run(q, st, block, pad=pad), *attended(q, clean, block, pad))
+
+
+@pytest.mark.parametrize("n", COUNTS)
+@pytest.mark.parametrize("kind", ("e4m3", "int8"))
+@pytest.mark.parametrize("power", (-60, -24, 40))
+@pytest.mark.parametrize("far", (-1e9, 1e9, torch.finfo(torch.float32).min))
+def test_far_pads_on_every_key_and_v_of_another_size(n, kind, power, far):
+    """Pads that absorb the scores absorb no scale of V: the row is the mean of V, whatever its size."""
+    B, H, N, d, block = 1, 2, 700, 64, 16
+    st = state(B, H, N, d, kind, block, 1), scaled(B, H, N, d, kind, block, 2, power)
+    q = rows((B, H, n, d), BF, 3)
+    pad = padded(B, N)
+    pad[:] = far
+    v = dense(*st[1], block)
+    # scores under 2^6 against a step of 2^7 of the pad in log2 units: nothing of them is left
+    want = [x.mean(2, keepdim=True).expand(B, H, n, d) for x in (v, v.abs(), v.abs())]
+    close(run(q, st, block, pad=pad), *want)
+
+
+@pytest.mark.parametrize("n, H, N", PLANS)
+@pytest.mark.parametrize("kind", ("e4m3", "int8"))
+@pytest.mark.parametrize("power", (-117, -100, 100, 120))
+@pytest.mark.parametrize("masked", (False, True))
+def test_v_near_the_ends_of_fp32(n, H, N, kind, power, masked):
+    """The row sums neither overflow nor vanish where every scale of V is tiny or huge."""
+    d, block = 96, 64
+    st = state(1, H, N, d, kind, block, 1), scaled(1, H, N, d, kind, block, 2, power)
+    q = rows((1, H, n, d), BF, 3)
+    pad = None
+    if masked:
+        pad = padded(1, N)
+        pad[:, N // 5: N // 3] = -math.inf
+    close(run(q, st, block, pad=pad), *attended(q, st, block, pad))
