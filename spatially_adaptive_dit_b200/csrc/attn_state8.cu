@@ -84,11 +84,12 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   return r;
 }
 
-// The value at shared-memory address `at` of the cluster's CTA `rank`.
-__device__ __forceinline__ float lds_of(uint32_t at, uint32_t rank) {
-  float v;
-  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-               : "=f"(v)
+// The values at shared-memory address `at` of the cluster's CTA `rank`.
+__device__ __forceinline__ float4 lds4_of(uint32_t at, uint32_t rank) {
+  float4 v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+               "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(at), "r"(rank)
                : "memory");
   return v;
@@ -117,8 +118,9 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   extern __shared__ __align__(16) uint8_t rows_smem[];
   __shared__ uint64_t full[C::NST], empty[C::NST];
   __shared__ int abort_word;
-  __shared__ float sm_m[kRowWarps][ROWS], sm_l[kRowWarps][ROWS], sm_range[kRowWarps][2];
-  __shared__ __align__(8) float cl_ml[ROWS][2], cl_range[2];  // of all warps, for the cluster
+  __shared__ float sm_m[kRowWarps][ROWS], sm_l[kRowWarps][ROWS], sm_a[kRowWarps], sm_range[kRowWarps][2];
+  __shared__ float4 cl_ml[ROWS];  // of all warps, for the cluster
+  __shared__ __align__(8) float cl_range[2];
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = blockIdx.x, tile = blockIdx.y, bh = blockIdx.z;
@@ -384,20 +386,20 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   if (__syncthreads_or(!ok) && !p.cluster) return;
 
   // ---- the warps' results joined in shared memory
-  float up = 1.f;
+  float up = 1.f, base_a = 0.f;
   if (warp < kRowWarps) {
     if (base != base) base = 0.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        up = leave_base(base, m[q][e], l[q][e]);
+        base_a = leave_base(base, l[q][e], up);
         l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 4);
         l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 8);
         l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 16);
         if (g == 0) sm_m[warp][8 * q + 2 * t + e] = m[q][e], sm_l[warp][8 * q + 2 * t + e] = l[q][e];
       }
-    if (lane == 0) sm_range[warp][0] = lv_lo, sm_range[warp][1] = lv_hi;
+    if (lane == 0) sm_a[warp] = base_a, sm_range[warp][0] = lv_lo, sm_range[warp][1] = lv_hi;
   }
   __syncthreads();
   // each warp's scaled output to the ring (its copies have all landed), added
@@ -409,10 +411,10 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * q + 2 * t + e;
-        float mx = -INFINITY;
+        RowRef ref;
 #pragma unroll
-        for (int v = 0; v < kRowWarps; ++v) mx = fmaxf(mx, sm_m[v][r]);
-        const float f = m[q][e] == -INFINITY ? 0.f : ex2_approx(m[q][e] - mx) * up;
+        for (int v = 0; v < kRowWarps; ++v) ref.take(sm_m[v][r], sm_a[v]);
+        const float f = ref.weight(m[q][e], base_a) * up;
         float* row = sm_part + (warp * ROWS + r) * D;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -429,20 +431,19 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
     return v;
   };
   for (int w = 0; w < kRowWarps; ++w) lv_lo = fminf(lv_lo, sm_range[w][0]), lv_hi = fmaxf(lv_hi, sm_range[w][1]);
-  float mx = -INFINITY, lx = 0.f;  // of row threadIdx.x
+  RowRef ref;
+  float lx = 0.f;  // of row threadIdx.x
   if (threadIdx.x < ROWS) {
-    for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, sm_m[w][threadIdx.x]);
-    for (int w = 0; w < kRowWarps; ++w) {  // (scores of NaN leave m at -inf and l at NaN, which stays)
-      const float mw = sm_m[w][threadIdx.x];
-      lx = fmaf(mw == -INFINITY ? 0.f : ex2_approx(mw - mx), sm_l[w][threadIdx.x], lx);
-    }
+    for (int w = 0; w < kRowWarps; ++w) ref.take(sm_m[w][threadIdx.x], sm_a[w]);
+    for (int w = 0; w < kRowWarps; ++w)  // (scores of NaN leave m at -inf and l at NaN, which stays)
+      lx = fmaf(ref.weight(sm_m[w][threadIdx.x], sm_a[w]), sm_l[w][threadIdx.x], lx);
   }
   if (p.cluster) {
     // ---- the parts joined by the cluster's CTAs: each takes its share of the
     // elements and adds the parts in their order
     float* const own = sm_part + kRowWarps * ROWS * D;
     for (int e = threadIdx.x; e < p.tile_rows * D; e += kRowThreads8) own[e] = joined(e);
-    if (threadIdx.x < ROWS) cl_ml[threadIdx.x][0] = mx, cl_ml[threadIdx.x][1] = lx;
+    if (threadIdx.x < ROWS) cl_ml[threadIdx.x] = make_float4(ref.m, lx, ref.a, 0.f);
     if (threadIdx.x == 0) cl_range[0] = lv_lo, cl_range[1] = lv_hi;
     rows_cluster_sync();
     const uint32_t own_s = smem_u32(own), ml_s = smem_u32(cl_ml), range_s = smem_u32(cl_range);
@@ -458,14 +459,18 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
       if (r >= p.n_rows) break;
       const int qi = p.idx ? __ldg(p.idx + r) : r;
       if (qi < 0 || qi >= p.Nq) continue;
-      float mm = -INFINITY;
+      RowRef all;
 #pragma unroll 4
-      for (int s = 0; s < p.n_split; ++s) mm = fmaxf(mm, lds_of(ml_s + uint32_t(rr * 8), s));
+      for (int s = 0; s < p.n_split; ++s) {
+        const float4 ml = lds4_of(ml_s + uint32_t(rr * 16), s);
+        all.take(ml.x, ml.z);
+      }
       float ls = 0.f, a0 = 0.f, a1 = 0.f;
 #pragma unroll 4
       for (int s = 0; s < p.n_split; ++s) {
-        const float2 ml = lds2_of(ml_s + uint32_t(rr * 8), s), x = lds2_of(own_s + uint32_t(e * 8), s);
-        const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
+        const float4 ml = lds4_of(ml_s + uint32_t(rr * 16), s);
+        const float2 x = lds2_of(own_s + uint32_t(e * 8), s);
+        const float w = all.weight(ml.x, ml.z);
         ls = fmaf(w, ml.y, ls);
         a0 = fmaf(w, x.x, a0);
         a1 = fmaf(w, x.y, a1);
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   if (p.n_split > 1) {
     const PartView pv = part_view(p, (int64_t(bh) * p.n_tiles + tile) * p.n_split + split, D);
     for (int e = threadIdx.x; e < p.tile_rows * D; e += kRowThreads8) pv.o[e] = joined(e);
-    if (threadIdx.x < p.tile_rows) pv.ml[threadIdx.x * 2] = mx, pv.ml[threadIdx.x * 2 + 1] = lx;
+    if (threadIdx.x < p.tile_rows) pv.ml[threadIdx.x] = make_float4(ref.m, lx, ref.a, 0.f);
     if (threadIdx.x == 0) pv.range[0] = lv_lo, pv.range[1] = lv_hi;
     return;
   }
@@ -508,13 +513,13 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
 
 // ------------------------------------------------------------- parts joined
 // One CTA for each query row: m = max m_i, out = sum 2^(m_i - m) O_i /
-// sum 2^(m_i - m) l_i over the row's parts.  Each warp takes every
+// sum 2^(m_i - m) l_i over the row's parts, m_i the reference of a part.  Each warp takes every
 // kJoinWarps-th part and the warps' sums are added in their order, so the
 // result does not depend on timing.  A few microseconds of dependent loads:
 // one thread per column over all parts in turn took 41 us at 200 parts.
 template <int D, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_state8_join_kernel(const __grid_constant__ State8Params p) {
-  __shared__ float sm_red[3][kJoinWarps], sm_l[kJoinWarps], sm_o[kJoinWarps][D];
+  __shared__ float sm_red[4][kJoinWarps], sm_l[kJoinWarps], sm_o[kJoinWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pu = blockIdx.x / p.tile_rows, rr = blockIdx.x - pu * p.tile_rows;
   const int unit = p.n_full + pu;
@@ -526,23 +531,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_state8_join_kernel(const
   if (qi < 0 || qi >= p.Nq) return;  // no row, or reported by the attention kernel
   const int n_rec = p.n_split << p.dual;
   const int64_t rec0 = int64_t(pu) * n_rec;
-  float m = -INFINITY, lo = INFINITY, hi = -INFINITY;
+  RowRef ref;
+  float lo = INFINITY, hi = -INFINITY;
   for (int s = threadIdx.x; s < n_rec; s += kJoinWarps * 32) {
     const PartView v = part_view(p, rec0 + s, D);
-    m = fmaxf(m, v.ml[rr * 2]);
+    const float4 ml = v.ml[rr];
+    ref.take(ml.x, ml.z);
     lo = fminf(lo, v.range[0]), hi = fmaxf(hi, v.range[1]);
   }
 #pragma unroll
   for (int e = 16; e; e >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
+    const float m = __shfl_xor_sync(0xffffffffu, ref.m, e), a = __shfl_xor_sync(0xffffffffu, ref.a, e);
+    ref.take(m, a);
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, e));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, e));
   }
-  if (lane == 0) sm_red[0][warp] = m, sm_red[1][warp] = lo, sm_red[2][warp] = hi;
+  if (lane == 0) sm_red[0][warp] = ref.m, sm_red[1][warp] = lo, sm_red[2][warp] = hi, sm_red[3][warp] = ref.a;
   __syncthreads();
+  ref = RowRef();  // in the warps' order, so that all take the same
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) {
-    m = fmaxf(m, sm_red[0][w]);
+    ref.take(sm_red[0][w], sm_red[3][w]);
     lo = fminf(lo, sm_red[1][w]), hi = fmaxf(hi, sm_red[2][w]);
   }
   float l = 0.f, acc[D / 32];
@@ -551,12 +560,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_state8_join_kernel(const
 #pragma unroll 4
   for (int s = warp; s < n_rec; s += kJoinWarps) {
     const PartView v = part_view(p, rec0 + s, D);
-    const float ms = v.ml[rr * 2], ls = v.ml[rr * 2 + 1];
+    const float4 ml = v.ml[rr];
     float x[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) x[e] = v.o[rr * D + lane + 32 * e];
-    const float w = ms == -INFINITY ? 0.f : ex2_approx(ms - m);
-    l = fmaf(w, ls, l);
+    const float w = ref.weight(ml.x, ml.z);
+    l = fmaf(w, ml.y, l);
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, x[e], acc[e]);
   }

@@ -115,13 +115,28 @@ __device__ __forceinline__ float query_factor(uint32_t max_bits, float scale, fl
 __device__ __forceinline__ float pow2(float e) { return __uint_as_float(uint32_t(127 + int(e)) << 23); }
 // The base of V scales from the log2 of the first one in use.
 __device__ __forceinline__ float scale_base(float lv) { return fminf(fmaxf(rintf(lv), -120.f), 120.f); }
-// Sums (m, l) relative to a base -> without it, and the factor of O that goes with
-// it: large bases leave by m and l and small ones by O, so neither overflows.
-__device__ __forceinline__ float leave_base(float base, float& m, float& l) {
-  m += fmaxf(base, 0.f);
-  l *= pow2(-fmaxf(base, 0.f));
-  return pow2(fminf(base, 0.f));
+// A row sum l relative to a base -> relative to `a`, which it returns, and the
+// factor of O that goes with it.  l takes what leaves it in range (at most 2^60),
+// O the rest.
+__device__ __forceinline__ float leave_base(float base, float& l, float& o_factor) {
+  const float a = fmaxf(base, -60.f);
+  l *= pow2(-a);
+  o_factor = pow2(base - a);
+  return a;
 }
+// The reference of a row's sums is 2^(m + a), kept apart: m may be the size of a
+// far pad, which absorbs a.
+struct RowRef {
+  float m = -INFINITY, a = 0.f;
+  // The larger one.
+  __device__ __forceinline__ void take(float m2, float a2) {
+    if ((m2 - m) + (a2 - a) > 0.f) m = m2, a = a2;
+  }
+  // Weight of sums that refer to (m2, a2); 0 of those without a key.
+  __device__ __forceinline__ float weight(float m2, float a2) const {
+    return m2 == -INFINITY ? 0.f : ex2_approx((m2 - m) + (a2 - a));
+  }
+};
 
 // A row came out as NaN: where its query row is finite, a NaN among the codes
 // (or the pads) did it.  Looked at where results leave, so that the loops over
@@ -134,21 +149,21 @@ __device__ __forceinline__ void report_nan(const State8Params& p, int b, int h, 
   set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
 }
 
-// A part's record: O [rows][D] unnormalised, (m, l) [rows], and the smallest
-// and largest log2 vs that it met (of all records behind one another).
+// A part's record: O [rows][D] unnormalised, (m, l, a, -) [rows], and the range
+// of V scales that it met (of all records behind one another).
 struct PartView {
   float* o;
-  float* ml;
+  float4* ml;
   float* range;
 };
 __host__ __device__ inline size_t part_floats(int64_t records, int rows, int D) {
-  return size_t(records) * (size_t(rows) * (D + 2) + 2);
+  return size_t(records) * (size_t(rows) * (D + 4) + 2);
 }
 __device__ __forceinline__ PartView part_view(const State8Params& p, int64_t rec, int D) {
   PartView v;
   v.o = p.part + rec * p.tile_rows * D;
-  v.ml = p.part + p.n_records * p.tile_rows * D + rec * p.tile_rows * 2;
-  v.range = p.part + p.n_records * p.tile_rows * (D + 2) + rec * 2;
+  v.ml = reinterpret_cast<float4*>(p.part + p.n_records * p.tile_rows * D) + rec * p.tile_rows;
+  v.range = p.part + p.n_records * p.tile_rows * (D + 4) + rec * 2;
   return v;
 }
 

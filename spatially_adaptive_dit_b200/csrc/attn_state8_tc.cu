@@ -585,11 +585,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (nan && live) report_nan(p, b, h, my_q, D);
         } else {
           const PartView pv = part_view(p, dual ? 2 * rest + t : rest, D);
-          const float up = leave_base(base, m_run, l_run);
-          if (live) {
-            pv.ml[rr * 2] = m_run;
-            pv.ml[rr * 2 + 1] = l_run;
-          }
+          float up;
+          const float base_a = leave_base(base, l_run, up);
+          if (live) pv.ml[rr] = make_float4(m_run, l_run, base_a, 0.f);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
 #pragma unroll

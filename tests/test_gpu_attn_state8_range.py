@@ -16,7 +16,7 @@ import pytest
 import torch
 
 from tests.gpu_util import sd
-from tests.test_gpu_attn_state8 import BF, dense, padded, run, state
+from tests.test_gpu_attn_state8 import BF, DEV, dense, padded, run, state
 from tests.test_gpu_rope import rows
 
 pytestmark = pytest.mark.gpu
@@ -153,3 +153,19 @@ def test_v_near_the_ends_of_fp32(n, H, N, kind, power, masked):
         pad = padded(1, N)
         pad[:, N // 5: N // 3] = -math.inf
     close(run(q, st, block, pad=pad), *attended(q, st, block, pad))
+
+
+@pytest.mark.parametrize("n, H, N", PLANS)
+@pytest.mark.parametrize("kind", ("e4m3", "int8"))
+@pytest.mark.parametrize("power", (-40, 0, 40))
+def test_far_pads_and_parts_that_start_at_different_scales(n, H, N, kind, power):
+    """Sums of a row that begin at scales of another size are joined as exactly under a far pad as without one."""
+    d, block = 96, 16
+    st = state(1, H, N, d, kind, block, 1), state(1, H, N, d, kind, block, 2)
+    vs = st[1][1]
+    vs *= torch.exp2(torch.randint(-3, 4, vs.shape, generator=torch.Generator().manual_seed(3)).float() + power).to(DEV)
+    q = rows((1, H, n, d), BF, 3)
+    pad = padded(1, N)
+    pad[:] = -1e9
+    v = dense(*st[1], block)
+    close(run(q, st, block, pad=pad), *(x.mean(2, keepdim=True).expand(1, H, n, d) for x in (v, v.abs(), v.abs())))
