@@ -428,14 +428,17 @@ safedit_status safedit_state8_store(const safedit_tensor *src,
  * safedit_attn_subset (there is no dense bias).  k8, v8 [B,H,Nk,d] codes of
  * one type, k_scale, v_scale [B,H,ceil(Nk/block)] f32, block in {16,32,64,128},
  * laid out as safedit_state8_store writes them.  Codes are widened exactly
- * and the sums are fp32; the probabilities alone are rounded (to f16).
+ * and the sums are fp32; the weights alone are rounded.  What that leaves of an
+ * element, before its rounding to bf16, is within 2^-11 sum_j p_j |V_j| +
+ * 2^-23 max_j(p_j) sum_j |V_j| of its sum, however the scales differ.
  *
  * A key with key_pad == -inf carries no weight whatever its codes and scales
  * hold.  The other keys' codes must not be NaN (safedit_state8_store writes
  * none), their pads neither NaN nor +inf, their scales must be finite,
  * k_scale >= 0, v_scale > 0, and those of one (b, h) slice of V within a
- * factor of 2^64 of each other; otherwise SAFEDIT_ERR_INVALID_ARG is set and
- * the rows are unspecified.  (NaN codes and pads are known by the rows that
+ * factor of 2^64 of each other (of 2^88 of a v_scale of exactly 1, as blocks of
+ * zeros have it); otherwise SAFEDIT_ERR_INVALID_ARG is set and the rows are
+ * unspecified.  (NaN codes and pads are known by the rows that
  * they make NaN, so a finite query row has to be among the call's.)
  * A row whose every key is masked sets SAFEDIT_ERR_MASKED_ROW and gets zeros.
  * A query row with a NaN comes out as NaN, with no status; the other rows do

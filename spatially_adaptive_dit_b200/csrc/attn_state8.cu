@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
   // queries 2 t and 2 t + 1 of each tile of eight
   float m[NQ][2], l[NQ][2];
   float lv_lo = INFINITY, lv_hi = -INFINITY;
-  float base = NAN;  // of this warp's V scales, NaN before the first
+  float base = NAN, lv_top = -INFINITY;  // of this warp's V scales (base: NaN before the first)
   bool ok = true;
   float o[NQ][NT][4];
 #pragma unroll
@@ -257,10 +257,11 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
         float lv = __log2f(vs);
         // finite, ks >= 0, vs > 0, by their bits
         bad |= __float_as_uint(ks) >= 0x7F800000u || __float_as_uint(vs) - 1u >= 0x7F7FFFFFu;
-        lv_lo = fminf(lv_lo, lv);
-        lv_hi = fmaxf(lv_hi, lv);
+        scale_range(vs, lv, lv_lo, lv_hi);
         if (base != base) base = scale_base(lv);
         lv -= base;
+        lv_top = fmaxf(lv_top, lv);
+        const bool wide = lv < lv_top - kHalfSpread || lv > kHalfSpread;
         float s[NQ][4];
 #pragma unroll
         for (int q = 0; q < NQ; ++q) s[q][0] = s[q][1] = s[q][2] = s[q][3] = 0.f;
@@ -304,8 +305,9 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
             if (key0 + g >= p.Nk) s[q][0] = s[q][1] = -INFINITY;
             if (key0 + g + 8 >= p.Nk) s[q][2] = s[q][3] = -INFINITY;
           }
-          up |= fmaxf(s[q][0], s[q][2]) + lv > m[q][0] + 8.f;
-          up |= fmaxf(s[q][1], s[q][3]) + lv > m[q][1] + 8.f;
+          // (as the exponents below, so that no weight leaves f16)
+          up |= (fmaxf(s[q][0], s[q][2]) - m[q][0]) + lv > kLazyTop;
+          up |= (fmaxf(s[q][1], s[q][3]) - m[q][1]) + lv > kLazyTop;
         }
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -316,6 +318,7 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              top -= kHeadroom;
               if (top > m[q][e]) {
                 const float al = ex2_approx(m[q][e] - top);  // 0 from m = -inf
                 m[q][e] = top;
@@ -330,16 +333,38 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
         }
         const float inv = ex2_approx(-lv);
         uint32_t bp[NQ][2];
+        // Wide: a group's weights go by their own largest, with the sums so far
+        // brought to that and back (16 keys of one scale are a step of the product).
+        float alone[NQ][2];
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float mm = m[q][e & 1] == -INFINITY ? 0.f : m[q][e & 1];
-            w[e] = ex2_approx((s[q][e] - mm) + lv);
+            s[q][e] = (s[q][e] - mm) + lv;
+            w[e] = ex2_approx(s[q][e]);
           }
           l[q][0] = fmaf(w[0] + w[2], inv, l[q][0]);
           l[q][1] = fmaf(w[1] + w[3], inv, l[q][1]);
+          if (wide) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(s[q][e], s[q][e + 2]);
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              top = fmaxf(rintf(top - kHeadroom), -88.f);
+              w[e] = ex2_approx(s[q][e] - top);
+              w[e + 2] = ex2_approx(s[q][e + 2] - top);
+              alone[q][e] = pow2(top);
+#pragma unroll
+              for (int c = 0; c < NT; ++c) {
+                o[q][c][e] *= pow2(-top);
+                o[q][c][e + 2] *= pow2(-top);
+              }
+            }
+          }
           bp[q][0] = transpose_8x8(pack_f16x2(w[0], w[1]));
           bp[q][1] = transpose_8x8(pack_f16x2(w[2], w[3]));
         }
@@ -374,6 +399,14 @@ __global__ void __launch_bounds__(kRowThreads8, RowsCfg<D>::CTAS)
             mma_16816(o[q][2 * c], a0, bp[q][0], bp[q][1]);
             mma_16816(o[q][2 * c + 1], a1, bp[q][0], bp[q][1]);
           }
+        }
+        if (wide) {
+#pragma unroll
+          for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[q][c][e] *= alone[q][e & 1];
         }
       }
       __syncwarp();

@@ -7,16 +7,28 @@
 //   out = sum_j p_j vs_j v8_j / sum_j p_j
 //
 // Scales never touch a code: ks goes into the score's factor, and vs into the
-// exponent of the weight w_j = 2^(t_j + lv_j - m), lv = log2 vs - base, m the
-// running maximum of t_j + lv_j.  So the weights that the tensor cores multiply
-// with the codes are at most 2^8 (with the lazy rescale) whatever the scales'
-// range, and f16 holds them to 2^-11; the row sum is sum_j w_j 2^-lv_j in fp32.
-// The base, the first scale in use to the nearest power of two, comes back with
-// the result.  It keeps lv small: a far pad absorbs it as it does the score, and
-// the sum must neither overflow nor vanish at scales near the ends of fp32.
-// Codes of both types are exact in f16, as is a bf16 query row after a power of
-// two has brought its largest element to 2^12 (elements 2^-29 below it lose
-// bits: 2^-36 of the row's largest), so the f16 weights are the only rounding.
+// exponent of the weight w_j = 2^(t_j + lv_j - m), lv = log2 vs - base, m 2^6
+// below the running maximum of t_j + lv_j, which it follows lazily, by more than
+// 2^8 at a time.  So the weights that the tensor cores multiply with the codes
+// are at most 2^14 whatever the scales' range; the row sum is
+// sum_j w_j 2^-lv_j in fp32.  The base, the first scale in use to the nearest
+// power of two, comes back with the result.  It keeps lv small: a far pad
+// absorbs it as it does the score, and the sum must neither overflow nor vanish
+// at scales near the ends of fp32.
+// A weight is rounded to f16: 2^-11, or, below 2^-14, 2^-25 in all, which is
+// 2^-31 of the row's largest p_j vs_j.  Where scales differ, that is no share of
+// the values that a small one stands for (a block of zeros beside rows of 1e-5
+// has a scale 2^25 times theirs).  So keys whose scale lies further than 2^8
+// below the largest so far are "wide" (and, with few rows, those as far above the
+// base: a far pad, which nothing takes off there, leaves lv as the weight).
+// With few rows their weights go by the largest of their own 16 keys; in the
+// tensor-core kernel a tile with such a key has its weights as a pair of bf16
+// (2^-16, to the end of fp32) and its codes of V as bf16.  Then 2^-23 max(p) |V_j|
+// of a key is all that is lost beside 2^-11 of its share.
+// Codes of both types are exact in f16 and bf16, as is a bf16 query row in f16
+// after a power of two has brought its largest element to 2^12 (elements 2^-29
+// below it lose bits: 2^-36 of the row's largest), so the weights alone are
+// rounded.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -57,6 +69,10 @@ struct State8Params {
 
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kScaleSpread = 64.f;  // log2 of the widest spread of V scales in one slice
+constexpr float kOneSlack = 24.f;     // and by how much more one of exactly 1 (of a block of zeros) may lie off
+constexpr float kHeadroom = 6.f;      // log2 of what a row's largest weight is at least ..
+constexpr float kLazyTop = 14.f;      // .. and at most, in f16's range
+constexpr float kHalfSpread = 8.f;    // V scales this near the largest (and the base) take f16 weights
 
 // pad in log2 units; a finite pad stays finite, so a row whose keys all carry
 // the type's lowest value averages them instead of being empty.
@@ -111,13 +127,31 @@ __device__ __forceinline__ float query_factor(uint32_t max_bits, float scale, fl
   return __uint_as_float(uint32_t(127 + f) << 23);
 }
 
+// f16x2 -> bf16x2 (exact for codes), two floats -> the bf16 pair that they begin
+// with and, in their place, what it leaves.
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t v) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return pack_bf16x2(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t take_bf16x2(float& lo, float& hi) {
+  const uint32_t r = pack_bf16x2(lo, hi);
+  lo -= __uint_as_float(r << 16);
+  hi -= __uint_as_float(r & 0xFFFF0000u);
+  return r;
+}
+
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float pow2(float e) { return __uint_as_float(uint32_t(127 + int(e)) << 23); }
+// The range of a slice's V scales, a scale's log2 at a time.
+__device__ __forceinline__ void scale_range(float vs, float lv, float& lo, float& hi) {
+  lo = fminf(lo, vs == 1.f ? kOneSlack : lv);
+  hi = fmaxf(hi, vs == 1.f ? -kOneSlack : lv);
+}
 // The base of V scales from the log2 of the first one in use.
 __device__ __forceinline__ float scale_base(float lv) { return fminf(fmaxf(rintf(lv), -120.f), 120.f); }
 // A row sum l relative to a base -> relative to `a`, which it returns, and the
 // factor of O that goes with it.  l takes what leaves it in range (at most 2^60),
-// O the rest.
+// O the rest: a block of zeros may have taken it 2^-88 below 1 already.
 __device__ __forceinline__ float leave_base(float base, float& l, float& o_factor) {
   const float a = fmaxf(base, -60.f);
   l *= pow2(-a);

@@ -18,6 +18,8 @@
 //     Q K_1(j+1), so one tile's softmax overlaps the other's MMAs.
 //   * online softmax in base 2 with a lazy rescale (by more than 2^8), scales
 //     of 16 keys at a time folded into the factor and offset of the exponent.
+//   * a tile with a wide key (see attn_state8.cuh) has pairs of bf16 weights and
+//     V as bf16, with a path of its own in each role.
 // With at most 128 query rows both tiles hold the same rows and take the key
 // tiles in turn, each with its own sums, which are joined like parts.
 //
@@ -37,6 +39,8 @@
 // Key tiles whose pads are all -inf are skipped by every role.  Every wait is
 // bounded; an expired one raises the CTA's abort flag, drains what is in
 // flight, frees TMEM and returns.
+#include <type_traits>
+
 #include "attn_state8.cuh"
 
 namespace sd {
@@ -62,12 +66,12 @@ struct TcCfg {
   static constexpr int N_BARS = 1 + 4 * NS + NR + 2 + 4 + 2;
   static constexpr int OFF_FACT = OFF_BAR + ((N_BARS * 8 + 8 + 15) / 16) * 16;
   static constexpr int OFF_BASE = OFF_FACT + NF * 8 * 12;  // of the V scales
-  static constexpr int OFF_PAD = OFF_BASE + 16;
+  static constexpr int OFF_FLAGS = OFF_BASE + 4;           // for each slot: bit 0 wide, bit 1 a masked key
+  static constexpr int OFF_PAD = OFF_BASE + ((4 + NF * 4 + 15) / 16) * 16;
   static constexpr int OFF_LIVE = OFF_PAD + NF * 128 * 4;
   static constexpr int OFF_TOP = OFF_LIVE + LIVE_WORDS * 4;  // the largest pad
-  static constexpr int OFF_DEAD = OFF_TOP + 4;               // for each slot: a key of the tile is masked
   static constexpr int SMEM_PLAIN = 1024 + OFF_PAD;
-  static constexpr int SMEM_PAD = 1024 + OFF_DEAD + NF * 4;
+  static constexpr int SMEM_PAD = 1024 + OFF_TOP + 4;
   static_assert(SMEM_PAD <= 232448, "shared memory");
   static_assert(8 * 32 * (2 * D + 16) <= OFF_RAW, "rows on their way out");
   static_assert(256 + 2 * D <= 512, "TMEM columns");
@@ -318,6 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{abort_flag, p.status, p.wait_limit};
+  auto flags_of = [&](int slot) { return __float_as_uint(lds32(sb + uint32_t(C::OFF_FLAGS + slot * 4))); };
 
   if (warp < 8) {
     // ================================================== softmax warpgroups
@@ -391,92 +396,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int n_mine = (live_count() - begin + step - 1) / step;
       int j = next_live(k_lo), slot = begin;
       if (begin && n_mine > 0) j = next_live(j + 1);
-      for (int it = 0; it < n_mine; ++it) {
-        if (!wait_warp(BAR(S_FULL + t), uint32_t(it & 1), ctl)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        float x[128];
-        {
-          uint32_t r[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + uint32_t(c * 32), r[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[c][e]);
-        }
-        // factors of the tile's eight groups of 16 keys: ks, log2 vs, 1 / vs
-        const uint32_t fact = sb + uint32_t(C::OFF_FACT + slot * 96);
-        const uint32_t pads = sb + uint32_t(C::OFF_PAD + slot * 512);
-        const int lim = p.Nk - j * C::BN;
-        const bool ragged = !PAD && lim < C::BN;
-        float kf[8], lv[8];
-#pragma unroll
-        for (int g = 0; g < 8; g += 4) {
-          const uint4 k4 = lds128(fact + uint32_t(g * 4)), l4 = lds128(fact + uint32_t(32 + g * 4));
-          kf[g] = undo * __uint_as_float(k4.x), kf[g + 1] = undo * __uint_as_float(k4.y);
-          kf[g + 2] = undo * __uint_as_float(k4.z), kf[g + 3] = undo * __uint_as_float(k4.w);
-          lv[g] = __uint_as_float(l4.x), lv[g + 1] = __uint_as_float(l4.y);
-          lv[g + 2] = __uint_as_float(l4.z), lv[g + 3] = __uint_as_float(l4.w);
-        }
-        tmem_wait_ld();
-        if constexpr (PAD) {  // exponents undo ks x + pad + log2 vs; kf and lv have done their part
-          // (the pads of 16 keys are read together: one read at a time, each
-          // waited for, cost a third of the tile)
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            uint4 pd[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pd[e] = lds128(pads + uint32_t(g * 64 + e * 16));
-            const uint64_t kf2 = f2_pack(kf[g], kf[g]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float* y = x + 16 * g + 4 * e;
-              f2_unpack(f2_fma(f2_pack(y[0], y[1]), kf2, f2_pack(__uint_as_float(pd[e].x), __uint_as_float(pd[e].y))),
-                        y[0], y[1]);
-              f2_unpack(f2_fma(f2_pack(y[2], y[3]), kf2, f2_pack(__uint_as_float(pd[e].z), __uint_as_float(pd[e].w))),
-                        y[2], y[3]);
-            }
-          }
-          if (far_pad != 0.f) {  // the pads here lack log2 vs
-            const uint64_t off = f2_pack(-far_pad, -far_pad);
-#pragma unroll
-            for (int c = 0; c < 128; c += 2) {
-              const float v = lv[c / 16];
-              f2_unpack(f2_add(f2_add(f2_pack(x[c], x[c + 1]), off), f2_pack(v, v)), x[c], x[c + 1]);
-            }
-          }
-#pragma unroll
-          for (int g = 0; g < 8; ++g) kf[g] = 1.f, lv[g] = 0.f;
-        } else if (ragged) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) x[c] = c < lim ? x[c] * kf[c / 16] : -INFINITY;
-#pragma unroll
-          for (int g = 0; g < 8; ++g) kf[g] = 1.f;
-        }
-        // The row's reference m follows the maximum lazily, by more than 2^8
-        // at a time.  (Taking the weights first and again where their sum says
-        // that m was too low saves the maximum, but keeps all 128 scores alive
-        // to the end: slower, for want of registers.)
-        float mt = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float* y = x + 16 * g;
-          float m0 = max3(y[0], y[1], y[2]), m1 = max3(y[3], y[4], y[5]);
-          m0 = max3(m0, y[6], y[7]), m1 = max3(m1, y[8], y[9]);
-          m0 = max3(m0, y[10], y[11]), m1 = max3(m1, y[12], y[13]);
-          m0 = max3(m0, y[14], y[15]);
-          mt = fmaxf(mt, fmaf(fmaxf(m0, m1), kf[g], lv[g]));
-        }
+      // The reference of the row's weights brought to a new maximum, with what was summed.
+      auto follow = [&](float mt, bool sums) {
         float alpha = 1.f;
         bool need_o = false;
-        if (mt > m_run + 8.f) {
-          alpha = ex2_approx(m_run - mt);  // 0 from m = -inf
+        if (mt > m_run + kLazyTop) {
+          const float to = mt - kHeadroom;
+          alpha = ex2_approx(m_run - to);  // 0 from m = -inf
           l_run *= alpha;
-          m_run = mt;
-          need_o = it > 0;
+          m_run = to;
+          need_o = sums;
         }
         if (__any_sync(0xffffffffu, need_o)) {
 #pragma unroll 1
@@ -489,38 +418,180 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tmem_st16(tO + uint32_t(e0), r);
           }
         }
-        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+      };
+      // A wide tile: pairs of bf16, 32 keys' in the columns of their scores, which are
+      // read 32 at a time and twice (few registers, so that the usual tile keeps its).
+      auto wide_tile = [&](uint32_t fact, uint32_t pads, int lim, bool sums) {
+        auto exponents = [&](int c, float (&a)[32]) {  // of 32 keys, without the reference
+          uint32_t r[32];
+          tmem_ld32(tS + uint32_t(c * 32), r);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 inv = lds64(fact + uint32_t(64 + c * 8));
-          uint32_t pk[16];
-#pragma unroll
-          for (int gg = 0; gg < 2; ++gg) {
-            const int g = 2 * c + gg;
-            const float off = lv[g] + neg_m;
-            const uint64_t kf2 = f2_pack(kf[g], kf[g]), off2 = f2_pack(off, off);
-            uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint64_t xx = f2_pack(x[16 * g + 2 * e], x[16 * g + 2 * e + 1]);
-              float a0, a1;
-              f2_unpack(PAD ? f2_add(xx, off2) : f2_fma(xx, kf2, off2), a0, a1);
-              const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
-              if (e & 1)
-                s1 = f2_add(s1, f2_pack(p0, p1));
-              else
-                s0 = f2_add(s0, f2_pack(p0, p1));
-              pk[8 * gg + e] = pack_f16x2(p0, p1);
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t at = fact + uint32_t((2 * c + e / 16) * 4);
+            const float k = undo * lds32(at), v = lds32(at + 32u), y = __uint_as_float(r[e]);
+            if constexpr (PAD) {
+              a[e] = fmaf(y, k, lds32(pads + uint32_t((32 * c + e) * 4)));
+              if (far_pad != 0.f) a[e] = (a[e] - far_pad) + v;
+            } else {
+              a[e] = 32 * c + e < lim ? fmaf(y, k, v) : -INFINITY;
             }
-            float u0, u1;
-            f2_unpack(f2_add(s0, s1), u0, u1);
-            l_run = fmaf(u0 + u1, gg ? inv.y : inv.x, l_run);
           }
-          tmem_st16(tS + uint32_t(c * 16), pk);
-          if (c & 1) {  // half of the keys: their products start
+        };
+        float mt = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float a[32];
+          exponents(c, a);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mt = fmaxf(mt, a[e]);
+        }
+        follow(mt, sums);
+        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float a[32];
+          exponents(c, a);
+          uint32_t w[16];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 16 * g; e < 16 * g + 16; ++e) {
+              a[e] = ex2_approx(a[e] + neg_m);
+              sum += a[e];
+            }
+            l_run = fmaf(sum, lds32(fact + uint32_t(64 + (2 * c + g) * 4)), l_run);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = take_bf16x2(a[2 * e], a[2 * e + 1]);
+          tmem_st16(tS + uint32_t(c * 32), w);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
+          tmem_st16(tS + uint32_t(c * 32 + 16), w);
+          if (c & 1) {
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(BAR(P_FULL + 2 * t + c / 2), lane);
+          }
+        }
+      };
+      for (int it = 0; it < n_mine; ++it) {
+        if (!wait_warp(BAR(S_FULL + t), uint32_t(it & 1), ctl)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // factors of the tile's eight groups of 16 keys: ks, lv, 2^-lv
+        const uint32_t fact = sb + uint32_t(C::OFF_FACT + slot * 96);
+        const uint32_t pads = sb + uint32_t(C::OFF_PAD + slot * 512);
+        const int lim = p.Nk - j * C::BN;
+        if (__any_sync(0xffffffffu, flags_of(slot) & 1u)) {
+          wide_tile(fact, pads, lim, it > 0);
+        } else {
+          float x[128];
+          {
+            uint32_t r[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + uint32_t(c * 32), r[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[c][e]);
+          }
+          const bool ragged = !PAD && lim < C::BN;
+          float kf[8], lv[8];
+#pragma unroll
+          for (int g = 0; g < 8; g += 4) {
+            const uint4 k4 = lds128(fact + uint32_t(g * 4)), l4 = lds128(fact + uint32_t(32 + g * 4));
+            kf[g] = undo * __uint_as_float(k4.x), kf[g + 1] = undo * __uint_as_float(k4.y);
+            kf[g + 2] = undo * __uint_as_float(k4.z), kf[g + 3] = undo * __uint_as_float(k4.w);
+            lv[g] = __uint_as_float(l4.x), lv[g + 1] = __uint_as_float(l4.y);
+            lv[g + 2] = __uint_as_float(l4.z), lv[g + 3] = __uint_as_float(l4.w);
+          }
+          tmem_wait_ld();
+          if constexpr (PAD) {  // exponents undo ks x + pad + log2 vs; kf and lv have done their part
+            // (the pads of 16 keys are read together: one read at a time, each
+            // waited for, cost a third of the tile)
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              uint4 pd[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) pd[e] = lds128(pads + uint32_t(g * 64 + e * 16));
+              const uint64_t kf2 = f2_pack(kf[g], kf[g]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float* y = x + 16 * g + 4 * e;
+                f2_unpack(f2_fma(f2_pack(y[0], y[1]), kf2, f2_pack(__uint_as_float(pd[e].x), __uint_as_float(pd[e].y))),
+                          y[0], y[1]);
+                f2_unpack(f2_fma(f2_pack(y[2], y[3]), kf2, f2_pack(__uint_as_float(pd[e].z), __uint_as_float(pd[e].w))),
+                          y[2], y[3]);
+              }
+            }
+            if (far_pad != 0.f) {  // the pads here lack log2 vs
+              const uint64_t off = f2_pack(-far_pad, -far_pad);
+#pragma unroll
+              for (int c = 0; c < 128; c += 2) {
+                const float v = lv[c / 16];
+                f2_unpack(f2_add(f2_add(f2_pack(x[c], x[c + 1]), off), f2_pack(v, v)), x[c], x[c + 1]);
+              }
+            }
+#pragma unroll
+            for (int g = 0; g < 8; ++g) kf[g] = 1.f, lv[g] = 0.f;
+          } else if (ragged) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) x[c] = c < lim ? x[c] * kf[c / 16] : -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) kf[g] = 1.f;
+          }
+          // The row's reference m follows the maximum lazily, by more than 2^8
+          // at a time.  (Taking the weights first and again where their sum says
+          // that m was too low saves the maximum, but keeps all 128 scores alive
+          // to the end: slower, for want of registers.)
+          float mt = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float* y = x + 16 * g;
+            float m0 = max3(y[0], y[1], y[2]), m1 = max3(y[3], y[4], y[5]);
+            m0 = max3(m0, y[6], y[7]), m1 = max3(m1, y[8], y[9]);
+            m0 = max3(m0, y[10], y[11]), m1 = max3(m1, y[12], y[13]);
+            m0 = max3(m0, y[14], y[15]);
+            mt = fmaxf(mt, fmaf(fmaxf(m0, m1), kf[g], lv[g]));
+          }
+          follow(mt, it > 0);
+          const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 inv = lds64(fact + uint32_t(64 + c * 8));
+            uint32_t pk[16];
+#pragma unroll
+            for (int gg = 0; gg < 2; ++gg) {
+              const int g = 2 * c + gg;
+              const float off = lv[g] + neg_m;
+              const uint64_t kf2 = f2_pack(kf[g], kf[g]), off2 = f2_pack(off, off);
+              uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint64_t xx = f2_pack(x[16 * g + 2 * e], x[16 * g + 2 * e + 1]);
+                float a0, a1;
+                f2_unpack(PAD ? f2_add(xx, off2) : f2_fma(xx, kf2, off2), a0, a1);
+                const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+                if (e & 1)
+                  s1 = f2_add(s1, f2_pack(p0, p1));
+                else
+                  s0 = f2_add(s0, f2_pack(p0, p1));
+                pk[8 * gg + e] = pack_f16x2(p0, p1);
+              }
+              float u0, u1;
+              f2_unpack(f2_add(s0, s1), u0, u1);
+              l_run = fmaf(u0 + u1, gg ? inv.y : inv.x, l_run);
+            }
+            tmem_st16(tS + uint32_t(c * 16), pk);
+            if (c & 1) {  // half of the keys: their products start
+              tmem_wait_st();
+              tc_fence_before();
+              warp_arrive(BAR(P_FULL + 2 * t + c / 2), lane);
+            }
           }
         }
         j = next_live(j + 1);
@@ -626,7 +697,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // descriptors in uniform registers: with a single lane in the loop each
       // of the 28 products of a tile took some 90 cycles to issue, which was
       // two thirds of the tile's time.
-      constexpr uint32_t idesc_qk = idesc_f16_f32(128, 128, 0), idesc_pv = idesc_f16_f32(128, D, 1);
+      constexpr uint32_t idesc_qk = idesc_f16_f32(128, 128, 0), idesc_pv = idesc_f16_f32(128, D, 1),
+                         idesc_pv_bf16 = idesc_bf16_f32(128, D, 0, 1);
       constexpr uint32_t SBO = 8u * C::ROWB;
       const uint64_t qd0 = smem_desc(sb, 16u, SBO, C::LAYOUT);
       const uint64_t kd0 = smem_desc(sb + C::OFF_K, 16u, SBO, C::LAYOUT);
@@ -645,13 +717,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_commit(BAR(S_FULL + t));
         }
       };
-      auto issue_pv = [&](int t, int hf, int s, bool acc) {  // half of the keys
+      auto issue_pv = [&](int t, int hf, int s, bool acc, bool wide) {  // half of the keys
         const uint64_t vd = vd0 + uint64_t(uint32_t(s * C::TILE_BYTES + hf * 64 * C::ROWB) >> 4);
-        if (elect_one()) {
+        const uint32_t to = tm + 256u + uint32_t(t * D), from = tm + uint32_t(t * 128);
+        if (wide) {  // a pair of bf16 each, where the scores were
+          if (elect_one()) {
+#pragma unroll 1
+            for (int kk = 0; kk < C::BN / 32; ++kk) {
+              const uint32_t pair = from + uint32_t((hf * 2 + kk / 2) * 32 + (kk & 1) * 8);
+              const uint64_t at = vd + (uint32_t(kk * 16 * C::ROWB) >> 4);
+              mma_ts(to, pair, at, idesc_pv_bf16, (acc || kk > 0) ? 1u : 0u);
+              mma_ts(to, pair + 16u, at, idesc_pv_bf16, 1u);
+            }
+          }
+        } else if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < C::BN / 32; ++kk)
-            mma_ts(tm + 256u + uint32_t(t * D), tm + uint32_t(t * 128 + hf * 32 + kk * 8),
-                   vd + (uint32_t(kk * 16 * C::ROWB) >> 4), idesc_pv, (acc || kk > 0) ? 1u : 0u);
+            mma_ts(to, from + uint32_t(hf * 32 + kk * 8), vd + (uint32_t(kk * 16 * C::ROWB) >> 4), idesc_pv,
+                   (acc || kk > 0) ? 1u : 0u);
         }
       };
       auto commit = [&](int bar) {
@@ -659,11 +742,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       const int n_live = live_count();
       // both halves of tile t's weights for its i-th key tile, as they come
-      auto weigh = [&](int t, int s, int i) {
+      auto weigh = [&](int t, int s, int i, bool wide) {
         for (int hf = 0; hf < 2; ++hf) {
           if (!wait_warp(BAR(P_FULL + 2 * t + hf), uint32_t(i & 1), ctl)) return false;
           tc_fence_after();
-          issue_pv(t, hf, s, i > 0 || hf > 0);
+          issue_pv(t, hf, s, i > 0 || hf > 0, wide);
         }
         return true;
       };
@@ -685,14 +768,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int ahead = dual ? 2 : 1, s1 = (j + ahead) % C::NS;
         const bool more = j + ahead < n_live;
         const int t = dual ? j & 1 : 0;
-        if (!(ok = weigh(t, s, dual ? j >> 1 : j))) break;
+        const bool wide = __shfl_sync(0xffffffffu, flags_of(j % C::NF), 0) & 1u;
+        if (!(ok = weigh(t, s, dual ? j >> 1 : j, wide))) break;
         if (dual) commit(V_EMPTY + s);
         if (more) {
           if (!(ok = keys_there(j + ahead))) break;
           issue_qk(t, s1);
         }
         if (!dual) {
-          if (two && !(ok = weigh(1, s, j))) break;
+          if (two && !(ok = weigh(1, s, j, wide))) break;
           commit(V_EMPTY + s);
           if (more && two) issue_qk(1, s1);
         }
@@ -732,17 +816,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sts128(a0, o[0], o[1], o[2], o[3]);
       sts128(a1, o[4], o[5], o[6], o[7]);
     };
-    // Rows of masked keys back to zero, whatever their codes (NaN) became.
-    // (int8 has no NaN: what it holds, a weight of 0 takes out.)
-    auto clear_dead = [&](uint32_t to, uint32_t pads) {
+    // What a tile rarely needs after its widening, row by row.  `clear`: rows of
+    // masked keys back to zero, whatever their codes (NaN) became.  (int8 has no
+    // NaN: what it holds, a weight of 0 takes out.)  `wide`: f16 -> bf16.
+    auto mend = [&](uint32_t to, uint32_t pads, bool clear, bool wide) {
 #pragma unroll 1
       for (int r = tid; r < C::BN; r += kTcWidenThreads) {
-        if (lds32(pads + uint32_t(r * 4)) != -INFINITY) continue;
+        bool zero = false;
+        if constexpr (PAD) zero = clear && lds32(pads + uint32_t(r * 4)) == -INFINITY;
+        if (!zero && !wide) continue;
 #pragma unroll 1
-        for (int c = 0; c < D / 8; ++c)
-          sts128(to + uint32_t((c * 8 / C::CH) * C::CHUNK_BYTES) +
-                     tc_swizzle(uint32_t(r * C::ROWB + (c * 8 % C::CH) * 2), C::LAYOUT),
-                 0u, 0u, 0u, 0u);
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t at = to + uint32_t((c * 8 / C::CH) * C::CHUNK_BYTES) +
+                              tc_swizzle(uint32_t(r * C::ROWB + (c * 8 % C::CH) * 2), C::LAYOUT);
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (!zero) {
+            v = lds128(at);
+            v = make_uint4(f16x2_to_bf16x2(v.x), f16x2_to_bf16x2(v.y), f16x2_to_bf16x2(v.z), f16x2_to_bf16x2(v.w));
+          }
+          sts128(at, v.x, v.y, v.z, v.w);
+        }
       }
     };
     constexpr int RPP = kTcWidenThreads / UPR;  // d = 64, 128: rows a pass
@@ -818,7 +911,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // group without one count for nothing, whatever they are.
     float next_ks = 0.f, next_vs = 1.f;
     float4 next_pad = make_float4(0.f, 0.f, 0.f, 0.f);
-    float base = NAN;  // of the V scales, NaN before the first in use
+    float base = NAN, lv_top = -INFINITY;  // of the V scales (base: NaN before the first in use)
     auto fetch = [&](int kt) {
       const int key = kt * C::BN + (lane & 7) * 16;
       if (key < p.Nk) {
@@ -851,8 +944,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!(ks >= 0.f && ks < INFINITY && next_vs > 0.f && next_vs < INFINITY)) {
           set_status(p.status, SAFEDIT_ERR_INVALID_ARG);
         } else {
-          lv_lo = fminf(lv_lo, lv);
-          lv_hi = fmaxf(lv_hi, lv);
+          scale_range(next_vs, lv, lv_lo, lv_hi);
         }
       }
       const uint32_t in_use = __ballot_sync(0xffffffffu, used) & 255u;
@@ -861,6 +953,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) sts32(sb + uint32_t(C::OFF_BASE), base);
       }
       if (used) lv -= base;
+      float most = used ? lv : -INFINITY, least = used ? lv : INFINITY;
+#pragma unroll
+      for (int e = 1; e < 8; e <<= 1) {
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, e));
+        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, e));
+      }
+      lv_top = fmaxf(lv_top, most);
+      uint32_t flags = least < lv_top - kHalfSpread ? 1u : 0u;
       if (lane < 8) {
         const uint32_t f = sb + uint32_t(C::OFF_FACT + slot * 96 + lane * 4);
         sts32(f, ks);
@@ -879,11 +979,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         sts128(sb + uint32_t(C::OFF_PAD + slot * 512 + lane * 16), __float_as_uint(pd[0]), __float_as_uint(pd[1]),
                __float_as_uint(pd[2]), __float_as_uint(pd[3]));
-        if constexpr (E4M3) {
-          dead = __any_sync(0xffffffffu, dead);
-          if (lane == 0) sts32(sb + uint32_t(C::OFF_DEAD + slot * 4), dead ? 1.f : 0.f);
-        }
+        if (E4M3 && __any_sync(0xffffffffu, dead)) flags |= 2u;
       }
+      if (lane == 0) sts32(sb + uint32_t(C::OFF_FLAGS + slot * 4), __uint_as_float(flags));
     };
     bool ok = true;
     int slot = 0, kt = next_live(k_lo);
@@ -898,8 +996,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int kt1 = next_live(kt + 1), slot1 = slot + 1 == C::NF ? 0 : slot + 1;
       const bool more = it + 1 < n_live;
       if (warp == 8 && more) fetch(kt1);
-      bool dead = false;  // a key of this tile is masked
-      if constexpr (PAD && E4M3) dead = lds32(sb + uint32_t(C::OFF_DEAD + slot * 4)) != 0.f;
+      const uint32_t flags = flags_of(slot);
+      const bool wide = flags & 1u, dead = PAD && E4M3 && (flags & 2u);
       for (int kv = 0; ok && kv < 2; ++kv) {
         const int n = 2 * it + kv, raw = n % C::NR;
         ok = wait_warp(BAR(RAW_FULL + raw), uint32_t((n / C::NR) & 1), ctl) &&
@@ -909,11 +1007,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (warp == 8 && kv && more) publish(kt1, slot1);
           widen(sb + uint32_t(C::OFF_RAW + raw * C::RAW_BYTES), to);
         }
-        if constexpr (PAD && E4M3) {
-          if (dead) {  // all three warps see the same, and come here whether or not a wait ran out
-            ok = !bar_any(2, kTcWidenThreads, !ok);
-            if (ok) clear_dead(to, sb + uint32_t(C::OFF_PAD + slot * 512));
-          }
+        if (dead || (kv && wide)) {  // all three warps see the same, and come here whether or not a wait ran out
+          ok = !bar_any(2, kTcWidenThreads, !ok);
+          if (ok) mend(to, sb + uint32_t(C::OFF_PAD + slot * 512), dead, kv && wide);
         }
         if (ok) {
           fence_proxy_async_smem();

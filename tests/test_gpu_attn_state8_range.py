@@ -4,8 +4,8 @@ Tolerance, per element, with A = sum_j p_j |v_j| and S = max_j(p_j) sum_j |v_j| 
   |got - out| <= 2^-8 |out| + (2^-11 + 2^-12) A + 2^-23 S
   - the result is rounded once to bf16: half a step, 2^-8 of the value;
   - every weight is rounded to f16 or finer (half a step, 2^-11 relative): at most 2^-11 A;
-  - f16's steps stop shrinking at 2^-14, where half a step is 2^-25 of the largest p_j vs_j, and the scales vs of the
-    keys in use lie within 2^2 of one another: 2^-23 max(p) of each |v|;
+  - f16's steps stop shrinking at 2^-14, where half a step is 2^-25.  The row's largest weight is 2^6 or more and an f16
+    weight belongs to a scale no further than 2^8 below the largest: 2^-25 2^-6 2^8 max(p) of each |v|;
   - scores of N(0,1) rows: under 2^-12 A (as in the tests of the ordinary range).
 Every term goes by the element's own values, so a row or a channel that lost its share of the sum is seen whatever
 the others hold.
@@ -15,8 +15,8 @@ import math
 import pytest
 import torch
 
-from tests.gpu_util import sd
-from tests.test_gpu_attn_state8 import BF, DEV, dense, padded, run, state
+from tests.gpu_util import expect_status, sd
+from tests.test_gpu_attn_state8 import BF, CODES, DEV, dense, padded, run, state
 from tests.test_gpu_rope import rows
 
 pytestmark = pytest.mark.gpu
@@ -153,6 +153,108 @@ def test_v_near_the_ends_of_fp32(n, H, N, kind, power, masked):
         pad = padded(1, N)
         pad[:, N // 5: N // 3] = -math.inf
     close(run(q, st, block, pad=pad), *attended(q, st, block, pad))
+
+
+def stored(x, kind, block):
+    """Codes and scales of x [B,H,N,d] as the store writes them."""
+    B, H, N, d = x.shape
+    codes = torch.zeros(B, H, N, d, dtype=torch.uint8, device=DEV).view(CODES[kind][0])
+    scales = torch.zeros(B, H, -(-N // block), device=DEV)
+    sd().safedit_state8_store([x], [codes], [scales], block)
+    expect_status(0)
+    return codes, scales
+
+
+@pytest.mark.parametrize("n", COUNTS)
+@pytest.mark.parametrize("kind, d, block", (("e4m3", 96, 32), ("int8", 64, 16), ("e4m3", 128, 64), ("int8", 96, 128)))
+@pytest.mark.parametrize("size", (1e-3, 1e-5, 3e-7, 1e-12, 1e-22))
+@pytest.mark.parametrize("zeros", ((0,), (3,), (0, 5)))
+@pytest.mark.parametrize("masked", (False, True))
+def test_small_rows_beside_blocks_of_zeros(n, kind, d, block, size, zeros, masked):
+    """Stored and attended: a block of zeros has the scale 1, which takes nothing from rows of 1e-3 to 1e-22 (nor does
+    the bound: a result of zeros is outside it nearly everywhere)."""
+    B, H, N = 1, 2, 1000
+    q, k = rows((B, H, n, d), BF, 1), rows((B, H, N, d), BF, 2)
+    v = (rows((B, H, N, d), BF, 3).float() * size).to(BF)
+    for i in zeros:
+        v[:, :, i * block: (i + 1) * block] = 0.0
+    st = stored(k, kind, block), stored(v, kind, block)
+    assert bool((st[1][1][:, :, list(zeros)] == 1.0).all())
+    pad = None
+    if masked:
+        pad = padded(B, N)
+        pad[:, 100:900:3] = -math.inf
+        pad[:, 2 * block: 3 * block] = -math.inf
+    want = attended(q, st, block, pad)
+    assert float((want[0].abs() > bound(*want)).double().mean()) > 0.95
+    close(run(q, st, block, pad=pad), *want)
+
+
+@pytest.mark.parametrize("n, H, N", PLANS)
+@pytest.mark.parametrize("kind", ("e4m3", "int8"))
+@pytest.mark.parametrize("power", (17, 20, 40))
+def test_one_outlier_of_v(n, H, N, kind, power):
+    """One element of 2^17 and more lifts its block's scale: the other channels keep what the other blocks hold there."""
+    d, block = 96, 32
+    q, k, v = (rows((1, H, m, d), BF, s) for s, m in enumerate((n, N, N)))
+    v[:, :, N // 3, 7] = 2.0 ** power
+    st = stored(k, kind, block), stored(v, kind, block)
+    want = attended(q, st, block)
+    others = [c for c in range(d) if c != 7]
+    # A result of zeros is seen.  Weights of N(0,1) scores have sum p^2 = e / N, so an element has the deviation
+    # (e / N)^(1/2), 9.5e-3 at 30000 keys, and A = 0.8: the bound's 6e-4 hides 2 * 0.4 * 6e-4 / 9.5e-3 = 5% of them
+    # there and less elsewhere.
+    assert float((want[0].abs() > bound(*want))[..., others].double().mean()) > 0.9
+    close(run(q, st, block), *want)
+
+
+@pytest.mark.parametrize("n, H, N", PLANS)
+@pytest.mark.parametrize("kind, d, block", (("e4m3", 96, 16), ("int8", 128, 32), ("e4m3", 64, 128), ("int8", 64, 64),
+                                            ("e4m3", 128, 16)))
+@pytest.mark.parametrize("order", ("random", "rising", "falling"))
+@pytest.mark.parametrize("masked", (False, True))
+def test_scales_over_the_whole_range(n, H, N, kind, d, block, order, masked):
+    """Blocks of V from 2^-30 to 2^30, in any order, each channel in use by one size of block alone, so that it shows
+    whether the small ones' shares are kept beside the large ones'."""
+    st = state(1, H, N, d, kind, block, 1), state(1, H, N, d, kind, block, 2)
+    (_, _), (v8, vs) = st
+    nb = vs.shape[2]
+    power = torch.linspace(-30.0, 30.0, nb) if nb > 1 else torch.zeros(1)
+    if order == "random":
+        power = power[torch.randperm(nb, generator=torch.Generator().manual_seed(nb))]
+    elif order == "falling":
+        power = power.flip(0)
+    vs *= torch.exp2(power.round()).to(DEV)
+    mine = ((power + 30.0) / 60.0 * d).long().clamp(0, d - 1)  # the channel from which on a block holds zeros
+    keep = torch.arange(d)[None, :] <= mine[:, None]
+    keep &= torch.arange(d)[None, :] > mine[:, None] - max(2, d // 8)
+    codes = v8.view(torch.uint8)
+    codes *= keep.to(DEV).repeat_interleave(block, 0)[:N].to(torch.uint8)
+    q = rows((1, H, n, d), BF, 3)
+    pad = None
+    if masked:
+        pad = padded(1, N)
+        pad.copy_(-torch.rand(1, N, generator=torch.Generator().manual_seed(3)))
+        pad[:, N // 5: N // 3] = -math.inf
+        pad[:, 1::5] = -math.inf
+    close(run(q, st, block, pad=pad), *attended(q, st, block, pad))
+
+
+@pytest.mark.parametrize("n", COUNTS)
+@pytest.mark.parametrize("kind", ("e4m3", "int8"))
+@pytest.mark.parametrize("order", ("rising", "falling"))
+def test_far_pads_and_scales_over_the_whole_range(n, kind, order):
+    """Where pads absorb every score the weights are the scales alone: the row is the mean of V still."""
+    B, H, N, d, block = 1, 2, 700, 64, 16
+    st = state(B, H, N, d, kind, block, 1), state(B, H, N, d, kind, block, 2)
+    vs = st[1][1]
+    power = torch.linspace(-30.0, 30.0, vs.shape[2]).round()
+    vs *= torch.exp2(power if order == "rising" else power.flip(0)).to(DEV)
+    q = rows((B, H, n, d), BF, 3)
+    pad = padded(B, N)
+    pad[:] = -1e9
+    v = dense(*st[1], block)
+    close(run(q, st, block, pad=pad), *(x.mean(2, keepdim=True).expand(B, H, n, d) for x in (v, v.abs(), v.abs())))
 
 
 @pytest.mark.parametrize("n, H, N", PLANS)
