@@ -265,7 +265,9 @@ _pack4, _pack3 = _TENSOR.pack, _TENSOR3.pack
 
 
 def _packed(t, device):
-    """`t` as the bytes of a safedit_tensor; it has to live on the current device (number `device`)."""
+    """`t` as the bytes of a safedit_tensor; it has to live on the current device (number `device`). None stays NULL."""
+    if t is None:
+        return None
     if t.get_device() != device:
         raise SafeditError(ERR_INVALID_ARG, f"a tensor on {t.device}, with cuda:{device} the current device")
     code = _DTYPE.get(t.dtype)
@@ -284,7 +286,10 @@ def _packed(t, device):
 
 
 def _packed_all(ts, device):
-    return b"".join([_packed(t, device) for t in ts])
+    try:
+        return b"".join([_packed(t, device) for t in ts])
+    except TypeError:
+        raise SafeditError(ERR_INVALID_ARG, "a sequence of tensors, without None") from None
 
 
 def _index_arg(idx, n_idx, device):
@@ -329,7 +334,7 @@ def safedit_state8_store(src, codes, scales, block, row0=0, idx=None, n_idx=0, s
     flags = None if rotate is None else struct.pack("%di" % len(src), *map(bool, rotate))
     _check(_lib.safedit_state8_store(_packed_all(src, dev), _packed_all(codes, dev), _packed_all(scales, dev), len(src),
                                      int(block), int(row0), _index_arg(idx, n_idx, dev), int(n_idx), int(src_indexed),
-                                     flags, None if pos is None else _packed(pos, dev), rope, _stream(stream)),
+                                     flags, _packed(pos, dev), rope, _stream(stream)),
            "safedit_state8_store")
 
 
@@ -345,7 +350,7 @@ def safedit_attn_subset_state8(q, k8, k_scale, v8, v_scale, block, idx, n_idx, k
         ptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(_lib.safedit_attn_subset_state8(_packed(q, dev), _packed(k8, dev), _packed(k_scale, dev), _packed(v8, dev),
                                            _packed(v_scale, dev), int(block), _index_arg(idx, n_idx, dev), int(n_idx),
-                                           None if key_pad is None else _packed(key_pad, dev), float(scale),
+                                           _packed(key_pad, dev), float(scale),
                                            _packed(out, dev), int(out_scattered), ptr, nbytes, _stream(stream)),
            "safedit_attn_subset_state8")
 
