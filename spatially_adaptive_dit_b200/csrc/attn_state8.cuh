@@ -120,7 +120,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // [2^12, 2^13), and its inverse times `scale`.
 __device__ __forceinline__ float query_factor(uint32_t max_bits, float scale, float& undo) {
   int e = int(max_bits >> 23) - 127;
-  if (max_bits == 0u) e = 12;  // a zero row
+  if (max_bits == 0u) e = -88;  // a zero row
   int f = 12 - e;
   f = f > 126 ? 126 : f;
   undo = scale * __uint_as_float(uint32_t(127 - f) << 23);

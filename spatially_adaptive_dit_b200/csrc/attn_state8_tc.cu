@@ -66,7 +66,7 @@ struct TcCfg {
   static constexpr int N_BARS = 1 + 4 * NS + NR + 2 + 4 + 2;
   static constexpr int OFF_FACT = OFF_BAR + ((N_BARS * 8 + 8 + 15) / 16) * 16;
   static constexpr int OFF_BASE = OFF_FACT + NF * 8 * 12;  // of the V scales
-  static constexpr int OFF_FLAGS = OFF_BASE + 4;           // for each slot: bit 0 wide, bit 1 a masked key
+  static constexpr int OFF_FLAGS = OFF_BASE + 4;  // for each slot its largest ks; sign: wide, lowest bit: a masked key
   static constexpr int OFF_PAD = OFF_BASE + ((4 + NF * 4 + 15) / 16) * 16;
   static constexpr int OFF_LIVE = OFF_PAD + NF * 128 * 4;
   static constexpr int OFF_TOP = OFF_LIVE + LIVE_WORDS * 4;  // the largest pad
@@ -94,6 +94,9 @@ constexpr uint64_t kTcDrainNs = 1000000000ull;
 // it, where the pad absorbs log2 vs and the score itself, as it does in the
 // plain sum, the largest pad comes off first.
 constexpr float kFarPad = 4096.f;
+// A row's factor of the products from which on scores may reach 2^22: products are
+// sums of at most 128 of a query of 2^13 and a code of 448.
+constexpr float kLargeFactor = 4194304.f / (8192.f * 448.f * 128.f);
 
 __device__ __forceinline__ uint32_t tc_swizzle(uint32_t off, uint32_t layout) {
   return layout == 2u ? (off ^ (((off >> 7) & 7u) << 4)) : (off ^ (((off >> 7) & 3u) << 4));
@@ -125,6 +128,12 @@ __device__ __forceinline__ void sts32(uint32_t at, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
+// Two weights -> f16x2; what rounding of a huge exponent takes past 65504 stays there.
+__device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // The larger ones of two pairs of bf16, NaN where one is.
 __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -419,9 +428,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       };
-      // A wide tile: pairs of bf16, 32 keys' in the columns of their scores, which are
-      // read 32 at a time and twice (few registers, so that the usual tile keeps its).
-      auto wide_tile = [&](uint32_t fact, uint32_t pads, int lim, bool sums) {
+      // A tile out of the ordinary: scores are read 32 at a time and twice (few
+      // registers, so that the usual tile keeps its).  `pair`: a wide one, pairs of
+      // bf16, 32 keys' in the columns of their scores.  Else one whose scores may be
+      // large: each exponent is rounded before the reference comes off, so that the
+      // largest one's does not depend on its size.  (The usual path takes a fused
+      // product, which at scores of 2^31 left the reference by 2^7.)
+      auto other_tile = [&](uint32_t fact, uint32_t pads, int lim, bool sums, bool pair) {
         auto exponents = [&](int c, float (&a)[32]) {  // of 32 keys, without the reference
           uint32_t r[32];
           tmem_ld32(tS + uint32_t(c * 32), r);
@@ -464,11 +477,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             l_run = fmaf(sum, lds32(fact + uint32_t(64 + (2 * c + g) * 4)), l_run);
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = take_bf16x2(a[2 * e], a[2 * e + 1]);
-          tmem_st16(tS + uint32_t(c * 32), w);
+          for (int e = 0; e < 16; ++e)
+            w[e] = pair ? take_bf16x2(a[2 * e], a[2 * e + 1]) : pack_f16x2_sat(a[2 * e], a[2 * e + 1]);
+          tmem_st16(tS + uint32_t(c * (pair ? 32 : 16)), w);
+          if (pair) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
-          tmem_st16(tS + uint32_t(c * 32 + 16), w);
+            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
+            tmem_st16(tS + uint32_t(c * 32 + 16), w);
+          }
           if (c & 1) {
             tmem_wait_st();
             tc_fence_before();
@@ -486,8 +502,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t fact = sb + uint32_t(C::OFF_FACT + slot * 96);
         const uint32_t pads = sb + uint32_t(C::OFF_PAD + slot * 512);
         const int lim = p.Nk - j * C::BN;
-        if (__any_sync(0xffffffffu, flags_of(slot) & 1u)) {
-          wide_tile(fact, pads, lim, it > 0);
+        const uint32_t flags = flags_of(slot);
+        if (__any_sync(0xffffffffu, flags >= 0x80000000u || !(__uint_as_float(flags) * undo < kLargeFactor))) {
+          other_tile(fact, pads, lim, it > 0, flags >> 31);
         } else {
           float x[128];
           {
@@ -768,7 +785,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int ahead = dual ? 2 : 1, s1 = (j + ahead) % C::NS;
         const bool more = j + ahead < n_live;
         const int t = dual ? j & 1 : 0;
-        const bool wide = __shfl_sync(0xffffffffu, flags_of(j % C::NF), 0) & 1u;
+        const bool wide = __shfl_sync(0xffffffffu, flags_of(j % C::NF), 0) >> 31;
         if (!(ok = weigh(t, s, dual ? j >> 1 : j, wide))) break;
         if (dual) commit(V_EMPTY + s);
         if (more) {
@@ -953,14 +970,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) sts32(sb + uint32_t(C::OFF_BASE), base);
       }
       if (used) lv -= base;
-      float most = used ? lv : -INFINITY, least = used ? lv : INFINITY;
+      float most = used ? lv : -INFINITY, least = used ? lv : INFINITY, top = ks;
 #pragma unroll
       for (int e = 1; e < 8; e <<= 1) {
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, e));
         least = fminf(least, __shfl_xor_sync(0xffffffffu, least, e));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
       }
       lv_top = fmaxf(lv_top, most);
-      uint32_t flags = least < lv_top - kHalfSpread ? 1u : 0u;
+      uint32_t flags = __float_as_uint(fmaxf(top, 0.f)) & 0x7FFFFFFEu;
+      if (least < lv_top - kHalfSpread) flags |= 0x80000000u;
       if (lane < 8) {
         const uint32_t f = sb + uint32_t(C::OFF_FACT + slot * 96 + lane * 4);
         sts32(f, ks);
@@ -979,7 +998,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         sts128(sb + uint32_t(C::OFF_PAD + slot * 512 + lane * 16), __float_as_uint(pd[0]), __float_as_uint(pd[1]),
                __float_as_uint(pd[2]), __float_as_uint(pd[3]));
-        if (E4M3 && __any_sync(0xffffffffu, dead)) flags |= 2u;
+        if (E4M3 && __any_sync(0xffffffffu, dead)) flags |= 1u;
       }
       if (lane == 0) sts32(sb + uint32_t(C::OFF_FLAGS + slot * 4), __uint_as_float(flags));
     };
@@ -997,7 +1016,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool more = it + 1 < n_live;
       if (warp == 8 && more) fetch(kt1);
       const uint32_t flags = flags_of(slot);
-      const bool wide = flags & 1u, dead = PAD && E4M3 && (flags & 2u);
+      const bool wide = flags >> 31, dead = PAD && E4M3 && (flags & 1u);
       for (int kv = 0; ok && kv < 2; ++kv) {
         const int n = 2 * it + kv, raw = n % C::NR;
         ok = wait_warp(BAR(RAW_FULL + raw), uint32_t((n / C::NR) & 1), ctl) &&

@@ -271,3 +271,46 @@ def test_far_pads_and_parts_that_start_at_different_scales(n, H, N, kind, power)
     pad[:] = -1e9
     v = dense(*st[1], block)
     close(run(q, st, block, pad=pad), *(x.mean(2, keepdim=True).expand(1, H, n, d) for x in (v, v.abs(), v.abs())))
+
+
+@pytest.mark.parametrize("n, H, N", PLANS)
+@pytest.mark.parametrize("kind", ("e4m3", "int8"))
+@pytest.mark.parametrize("size", (1e3, 1e5, 1e7, 1e9))
+@pytest.mark.parametrize("masked", (False, True))
+def test_scores_far_beyond_the_exponents_steps(n, H, N, kind, size, masked):
+    """Scores of 1e3 to 1e9: a key that leads the others of its row by more than fp32 leaves uncertain has all of the
+    weight (no weight leaves f16's range on the way), and every row stays within what V holds."""
+    d, block = 96, 64
+    st = state(1, H, N, d, kind, block, 1), state(1, H, N, d, kind, block, 2)
+    q = (rows((1, H, n, d), BF, 3).float() * size).to(BF)
+    pad = None
+    if masked:
+        pad = padded(1, N)
+        pad[:, N // 5: N // 3] = -math.inf
+    got = run(q, st, block, pad=pad).double().cpu()
+    k, v = dense(*st[0], block), dense(*st[1], block)
+    t = q.double().cpu() @ k.transpose(2, 3) * d ** -0.5
+    if pad is not None:
+        t = t.masked_fill(pad.cpu()[:, None, None, :] == -math.inf, -math.inf)
+    two, at = t.topk(2, -1)
+    # a score's products and their sum in fp32: 96 terms of 4 size each, 2^-24 of their absolute sum, twice over; and the
+    # exponent's sum, 2^-24 of the score.  40 beyond that leaves e^-40 N.
+    sure = two[..., 0] - two[..., 1] > 40.0 + 2.0 ** -22 * (96 * 4 * size * d ** -0.5 + two[..., 0].abs())
+    assert bool(sure.any()) or size < 1e5
+    best = v.gather(2, at[..., :1].expand(1, H, n, d))
+    # the key's weight is rounded to f16 where the row's sum has it in fp32: 2^-11, then the result to bf16
+    assert bool(((got - best).abs() <= (2.0 ** -8 + 2.0 ** -11 * (1 + 2.0 ** -8)) * best.abs() + 1e-12)[sure].all())
+    assert bool((got.abs() <= 1.01 * v.abs().amax(2, keepdim=True)).all())
+
+
+@pytest.mark.parametrize("n", COUNTS)
+def test_k_scales_of_zero_beside_v_scales_of_every_size(n):
+    """K of zeros (k_scale 0 too): every key counts alike, whatever the scales of V."""
+    B, H, N, d, block = 1, 2, 700, 64, 16
+    st = state(B, H, N, d, "e4m3", block, 1), state(B, H, N, d, "e4m3", block, 2)
+    st[0][1].zero_()
+    vs = st[1][1]
+    vs *= torch.exp2(torch.linspace(-30.0, 30.0, vs.shape[2]).flip(0).round()).to(DEV)
+    q = rows((B, H, n, d), BF, 3)
+    q[:, :, 0] = 0.0
+    close(run(q, st, block), *attended(q, st, block))
