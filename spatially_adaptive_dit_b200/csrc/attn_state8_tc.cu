@@ -128,6 +128,12 @@ __device__ __forceinline__ void sts32(uint32_t at, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
+// The warp's largest.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 // Two weights -> f16x2; what rounding of a huge exponent takes past 65504 stays there.
 __device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi) {
   uint32_t r;
@@ -503,7 +509,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t pads = sb + uint32_t(C::OFF_PAD + slot * 512);
         const int lim = p.Nk - j * C::BN;
         const uint32_t flags = flags_of(slot);
-        if (__any_sync(0xffffffffu, flags >= 0x80000000u || !(__uint_as_float(flags) * undo < kLargeFactor))) {
+        const bool other = flags >= 0x80000000u || !(__uint_as_float(flags) * undo < kLargeFactor);
+        if (__builtin_expect(__any_sync(0xffffffffu, other), 0)) {
           other_tile(fact, pads, lim, it > 0, flags >> 31);
         } else {
           float x[128];
@@ -737,7 +744,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       auto issue_pv = [&](int t, int hf, int s, bool acc, bool wide) {  // half of the keys
         const uint64_t vd = vd0 + uint64_t(uint32_t(s * C::TILE_BYTES + hf * 64 * C::ROWB) >> 4);
         const uint32_t to = tm + 256u + uint32_t(t * D), from = tm + uint32_t(t * 128);
-        if (wide) {  // a pair of bf16 each, where the scores were
+        if (__builtin_expect(wide, 0)) {  // a pair of bf16 each, where the scores were
           if (elect_one()) {
 #pragma unroll 1
             for (int kk = 0; kk < C::BN / 32; ++kk) {
@@ -970,16 +977,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) sts32(sb + uint32_t(C::OFF_BASE), base);
       }
       if (used) lv -= base;
-      float most = used ? lv : -INFINITY, least = used ? lv : INFINITY, top = ks;
-#pragma unroll
-      for (int e = 1; e < 8; e <<= 1) {
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, e));
-        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, e));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-      }
-      lv_top = fmaxf(lv_top, most);
-      uint32_t flags = __float_as_uint(fmaxf(top, 0.f)) & 0x7FFFFFFEu;
-      if (least < lv_top - kHalfSpread) flags |= 0x80000000u;
+      lv_top = fmaxf(lv_top, warp_max(used ? lv : -INFINITY));
+      uint32_t flags = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(ks, 0.f))) & 0x7FFFFFFEu;
+      if (__any_sync(0xffffffffu, used && lv < lv_top - kHalfSpread)) flags |= 0x80000000u;
       if (lane < 8) {
         const uint32_t f = sb + uint32_t(C::OFF_FACT + slot * 96 + lane * 4);
         sts32(f, ks);
@@ -1023,16 +1023,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
              wait_warp(BAR((kv ? V_EMPTY : K_EMPTY) + s), ph, ctl);
         const uint32_t to = sb + uint32_t((kv ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES);
         if (ok) {
-          if (warp == 8 && kv && more) publish(kt1, slot1);
           widen(sb + uint32_t(C::OFF_RAW + raw * C::RAW_BYTES), to);
         }
-        if (dead || (kv && wide)) {  // all three warps see the same, and come here whether or not a wait ran out
+        if (__builtin_expect(dead || (kv && wide), 0)) {  // all three warps see the same, and come here whether or not a wait ran out
           ok = !bar_any(2, kTcWidenThreads, !ok);
           if (ok) mend(to, sb + uint32_t(C::OFF_PAD + slot * 512), dead, kv && wide);
         }
         if (ok) {
           fence_proxy_async_smem();
           warp_arrive(BAR((kv ? V_FULL : K_FULL) + s), lane);
+          if (warp == 8 && kv && more) publish(kt1, slot1);
         }
         ok = !bar_any(1, kTcWidenThreads, !ok);  // read by all three warps, or given up by all
         if (ok && tid == 0) load_next();
