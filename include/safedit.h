@@ -383,7 +383,8 @@ safedit_status safedit_rope_rows(const safedit_tensor *src,
  * qmax = 448 (e4m3) or 127 (int8); m = 0 takes scale 1, and 0 < m < 2^-100
  * counts as 2^-100.  x is the source element, rotated first (in fp32, as
  * safedit_rope_rows does, with no rounding in between) in the tensors with
- * host_rotate[t] == 1.
+ * host_rotate[t] == 1.  The quotient is fp32: an f32 or a rotated element within
+ * 2^-22 of the border between two codes may take either.
  *
  * For t < n_tensors, r < n, i = d_idx ? d_idx[r] : r:
  *   state row row0 + r = src[t][b,h,(src_indexed ? i : r),:]  at pos[b,i,:]

@@ -24,9 +24,10 @@ namespace sd {
 //   out^T = V^T W^T: the weights' 8 x 8 blocks are transposed between the
 //     lanes; the lane loads, of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, the
 //     elements of column group g, and interleaves them by bytes.
-// One row over 25600 keys of 48 slices (d = 96, 236 MB): 46.6 us, 5.1 TB/s, in
-// clusters of eight (42 us and a join of 5 in nine parts), against 107 us with the codes straight from global
-// memory into registers (a group of keys ahead was all that fitted).
+// One row over 25600 keys of 48 slices (d = 96, 236 MB): 45 to 48 us, 5.1 TB/s,
+// in clusters of eight (42 us and a join of 5 in nine parts), against 107 us with
+// the codes straight from global memory into registers (a group of keys ahead was
+// all that fitted).  A slice whose scales are wide throughout takes 53 us.
 // The copies' 128-byte (d = 128) or 64-byte (d = 64) swizzle keeps those reads
 // off each other's banks; rows of 96 bytes are so by themselves.
 constexpr int kRowWarps = 4;                         // warps that multiply
@@ -637,8 +638,9 @@ static int state8_sms() {
   return sms;
 }
 
-// Rows of a slice up to which the warp-level kernel is taken.  Measured, us,
-// warp-level / tensor-core kernel: 48 slices x 25600 keys of 96: 16 rows 64 /
+// Rows of a slice up to which the warp-level kernel is taken.  Measured when the
+// rule was made (both are some 7% slower since they look at the scales' range:
+// 32 rows 113, 48 rows 128), us, warp-level / tensor-core kernel: 48 slices x 25600 keys of 96: 16 rows 64 /
 // 120, 32 rows 108 / 118, 48 rows 148 / 122; x 4096 keys: 16 rows 23 / 33, 32
 // rows 30 / 33, 48 rows 37 / 36; 32 slices x 16384 keys of 128: 32 rows 70 /
 // 76, 48 rows 91 / 76; 4 slices x 4096 of 96: 32 rows 19 / 25.
@@ -667,7 +669,7 @@ static State8Plan plan_state8(int64_t n_rows, int64_t BH, int64_t Nk, int D, int
     // as the GPU holds at once (clusters of two to eight fill 86.5% of its
     // places or more; nine for 48 slices left some for a second wave, 65 us
     // against 47).  The launch that this saves is worth twelve stages or so.
-    // Measured in a captured graph, us, cluster / join: 24 slices x 4999 keys of
+    // Measured in a captured graph when the rule was made, us, cluster / join: 24 slices x 4999 keys of
     // 64, 13 rows 14.0 / 15.0; 48 x 1000 of 96, 13 rows 10.5 / 13.1; 8 x 512 of
     // 96 5.9 / 7.5 (whole); 4 x 9000 of 128, 20 rows 21.8 / 15.5; launched one
     // by one, where a launch is the host's time: 48 x 25600 of 96, one row 46.6

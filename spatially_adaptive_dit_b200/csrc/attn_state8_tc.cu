@@ -29,13 +29,16 @@
 // 2048 where the two tiles meet) against 1536 of tensor time; at d = 128 the
 // tensor time is 2048 and the widening of int8 codes (two instructions a pair
 // and an exclusive or, against one conversion of e4m3) shows too.  One wave of
-// 148 CTAs over 8192 keys, us (TFLOP/s): d = 64 127 (620), d = 96 127 / 133
-// (940 / 890, e4m3 / int8), d = 128 139 / 151 (1140 / 1050); the same shapes
-// over a bf16 state take 125 at d = 96.  Measured and not kept: two
-// warpgroups to a tile (24 warps, 80 registers; 154 against 127), halves of
-// the keys with their own score products (N = 64 products read the query tile
-// twice and run at 48 cycles instead of 32; 169 against 139 at d = 128),
-// 1/8 or 1/4 of the exponentials as a polynomial (126 to 131 against 127).
+// 148 CTAs over 8192 keys, us (TFLOP/s), e4m3 / int8: d = 64 120 / 126 (660 /
+// 630), d = 96 130 / 136 (915 / 875), d = 128 147 / 162 (1080 / 980), with pads
+// 161 / 163, 170 / 178, 183 / 206; the same shapes over a bf16 state take 125 at
+// d = 96.  The paths for wide tiles and large scores, not taken there, cost 5% of
+// this (123 / 129 and 140 / 151 without them): registers and code beside the
+// usual tile's.  Taken, they take 2.3 times as long.  Measured, before them, and
+// not kept: two warpgroups to a tile (24 warps, 80 registers; 154 against 127),
+// halves of the keys with their own score products (N = 64 products read the
+// query tile twice and run at 48 cycles instead of 32; 169 against 139 at d =
+// 128), 1/8 or 1/4 of the exponentials as a polynomial (126 to 131 against 127).
 // Key tiles whose pads are all -inf are skipped by every role.  Every wait is
 // bounded; an expired one raises the CTA's abort flag, drains what is in
 // flight, frees TMEM and returns.
@@ -80,8 +83,8 @@ struct TcCfg {
 constexpr int kTcThreads = 384;
 constexpr int kTcWidenThreads = 96;
 // 256 * 208 + 128 * 88 = 256 * 192 + 128 * 120 = 384 * 168.  The second split
-// is the pads' (8192 keys of 96, e4m3: 160 us against 183 with the first,
-// which spills there; without pads 130 against 127).
+// is the pads' (8192 keys of 96, e4m3, when it was chosen: 160 us against 183
+// with the first, which spills there; without pads 130 against 127).
 template <bool PAD>
 struct TcRegs {
   static constexpr uint32_t SOFTMAX = PAD ? 192 : 208, OTHER = PAD ? 120 : 88;

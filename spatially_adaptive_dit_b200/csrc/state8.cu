@@ -9,8 +9,12 @@
 // in registers, reads it once, and walks the heads of its group with the
 // angles of its tokens kept, the next heads' loads in flight while this one
 // is reduced (one barrier for each head).  K and V of 25600 tokens x 48 heads
-// of 96 (708 MB): 145 us with K rotated, 128 us without (blocks of 64); d =
-// 128: 170 and 156 us, 5.5 and 6.0 TB/s.
+// of 96 (708 MB): 140 to 150 us with K rotated, 128 us without (blocks of 64);
+// d = 128: 170 and 156 us, 5.5 and 6.0 TB/s.
+//
+// The arithmetic is fp32's: an f32 or a rotated element within 2^-22 of the
+// border between two codes may take either one, a 16-bit one that is not rotated
+// meets every border as it is.
 #include <type_traits>
 
 #include <cuda_fp16.h>
@@ -301,9 +305,11 @@ template <typename T, int BLOCK, bool HALVES>
 static safedit_status launch_store(StoreParams& p, int64_t B, int64_t n_heads, int n_tensors, cudaStream_t s) {
   const int threads = StoreCfg<BLOCK>::RP * p.slots;
   const int64_t blocks = (int64_t(p.n_rows) + BLOCK - 1) / BLOCK;
-  // as few head groups as still give every SM 2048 threads: each pays for the
-  // angles again (25600 rows x 48 heads of 96, blocks of 64, measured at 154 us: with
-  // twice the groups 164, four times 193)
+  // Head groups by a count of 2048 threads an SM: each pays for the angles again
+  // (25600 rows x 48 heads of 96, blocks of 64, when the call took 154 us: with twice
+  // the groups 164, four times 193).  The registers of blocks of 32 and more admit
+  // fewer (at d = 96 four blocks of 192 threads, or two from blocks of 64 on), so a
+  // short call runs in more waves than this counts.
   const int64_t ctas = 148 * (2048 / threads);
   int64_t want = (ctas + blocks * B - 1) / (blocks * B);
   p.heads_per_group = int((n_heads + want - 1) / want);
