@@ -314,3 +314,78 @@ def test_k_scales_of_zero_beside_v_scales_of_every_size(n):
     q = rows((B, H, n, d), BF, 3)
     q[:, :, 0] = 0.0
     close(run(q, st, block), *attended(q, st, block))
+
+
+@pytest.mark.parametrize("n, H, N", ((1, 300, 2000), (12, 44, 6000), (40, 3, 2000), (100, 3, 2000), (300, 3, 2000)))
+@pytest.mark.parametrize("kind", ("e4m3", "int8"))
+@pytest.mark.parametrize("masked", (False, True))
+def test_waits_that_run_out_among_wide_keys(n, H, N, kind, masked):
+    """With no time to wait every role gives up on tiles of small V scales too: reported, and the next call gives the
+    first one's bits."""
+    d, block = 96, 64
+    st = state(1, H, N, d, kind, block, 1), state(1, H, N, d, kind, block, 2)
+    st[1][1][:, :, ::3] *= 2.0 ** 20
+    q = rows((1, H, n, d), BF, 3)
+    pad = None
+    if masked:
+        pad = padded(1, N)
+        pad[:, 5::7] = -math.inf
+    first = run(q, st, block, pad=pad)
+    old = sd().safedit_debug_set_wait_limit_ns(0)
+    try:
+        run(q, st, block, pad=pad, status=sd().ERR_TIMEOUT)
+    finally:
+        sd().safedit_debug_set_wait_limit_ns(old)
+    again = run(q, st, block, pad=pad)
+    assert torch.equal(first, again)
+    close(again, *attended(q, st, block, pad))
+
+
+@pytest.mark.parametrize("n", COUNTS)
+def test_wide_keys_in_two_graphs_with_workspaces_of_their_own(n):
+    """Captured and replayed in turn on new inputs, wide and ordinary slices beside each other."""
+    B, H, N, d, block = 1, 3, 3000, 64, 32
+    sets = []
+    for s in (1, 2):
+        st = state(B, H, N, d, "e4m3", block, s), state(B, H, N, d, "e4m3", block, s + 5)
+        st[1][1][:, s, 7::9] *= 2.0 ** 18
+        q = rows((B, H, n, d), BF, s)
+        out = torch.zeros(B, H, n, d, dtype=BF, device=DEV)
+        size = sd().safedit_attn_subset_state8_workspace_size(B, H, n, N, d)
+        ws = torch.empty(size, dtype=torch.uint8, device=DEV) if size else None
+        (k8, ks), (v8, vs) = st
+        call = lambda q=q, k8=k8, ks=ks, v8=v8, vs=vs, out=out, ws=ws: sd().safedit_attn_subset_state8(  # noqa: E731
+            q, k8, ks, v8, vs, block, None, 0, None, 0.0, out, 0, ws)
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        sets.append((q, st, out, graph))
+    for q, st, out, graph in sets:
+        q.copy_(q.flip(2) * 0.5)
+        st[1][1].copy_(st[1][1].flip(2))
+        out.zero_()
+    for _ in range(2):
+        for *_, graph in sets:
+            graph.replay()
+    torch.cuda.synchronize()
+    expect_status(0)
+    for q, st, out, _ in sets:
+        close(out, *attended(q, st, block))
+
+
+@pytest.mark.parametrize("n, H, N", PLANS)
+@pytest.mark.parametrize("power, status", ((-78, 0), (-88, 1), (88, 0), (100, 1)))
+def test_how_far_a_scale_of_one_may_lie_off(n, H, N, power, status):
+    """A block of zeros (scale 1) within 2^88 of the others takes nothing from them; farther off it is reported."""
+    d, block = 96, 64
+    st = state(1, H, N, d, "e4m3", block, 1), scaled(1, H, N, d, "e4m3", block, 2, power)
+    codes, scales = st[1]
+    codes.view(torch.uint8)[:, :, block: 2 * block] = 0
+    scales[:, :, 1] = 1.0
+    q = rows((1, H, n, d), BF, 3)
+    if status:
+        run(q, st, block, status=sd().ERR_INVALID_ARG)
+    else:
+        close(run(q, st, block), *attended(q, st, block))
