@@ -91,10 +91,10 @@ struct TcRegs {
   static_assert(256 * SOFTMAX + 128 * OTHER <= 384 * 168, "register split");
 };
 constexpr uint64_t kTcDrainNs = 1000000000ull;
-// A batch whose largest pad is within this (in log2 units) has log2 vs added to
+// A batch whose largest pad is within this (in log2 units) has lv added to
 // its pads: a sum that matters is off by 2^-13 at most, within the weights' f16
 // rounding (keys 2^13 below the largest have no weight either way).  Beyond
-// it, where the pad absorbs log2 vs and the score itself, as it does in the
+// it, where the pad absorbs lv and the score itself, as it does in the
 // plain sum, the largest pad comes off first.
 constexpr float kFarPad = 4096.f;
 // A row's factor of the products from which on scores may reach 2^22: products are
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             lv[g + 2] = __uint_as_float(l4.z), lv[g + 3] = __uint_as_float(l4.w);
           }
           tmem_wait_ld();
-          if constexpr (PAD) {  // exponents undo ks x + pad + log2 vs; kf and lv have done their part
+          if constexpr (PAD) {  // exponents undo ks x + pad + lv; kf and lv have done their part
             // (the pads of 16 keys are read together: one read at a time, each
             // waited for, cost a third of the tile)
 #pragma unroll
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                           y[2], y[3]);
               }
             }
-            if (far_pad != 0.f) {  // the pads here lack log2 vs
+            if (far_pad != 0.f) {  // the pads here lack lv
               const uint64_t off = f2_pack(-far_pad, -far_pad);
 #pragma unroll
               for (int c = 0; c < 128; c += 2) {
